@@ -25,6 +25,7 @@ GALE_ERR_SELFTEST = -7
 GALE_F32, GALE_BF16, GALE_F16 = 0, 1, 2
 GALE_MODE_PLAIN, GALE_MODE_SWIGLU = 0, 1
 GALE_FLAG_RESIDUAL_RMSNORM = 1
+GALE_SCORE_SOFTMAX, GALE_SCORE_SIGMOID = 0, 1
 
 # every symbol include/gale.h declares
 EXPORTS = (
@@ -36,6 +37,8 @@ EXPORTS = (
     "gale_debug_set_failure", "gale_route_topk",
     "gale_w4_layout", "gale_w4_quantize", "gale_w4_workspace_size", "gale_w4_gemv", "gale_encode",
     "gale_moe_chain", "gale_moe_chain_workspace_size", "gale_expert_forward", "gale_expert_forward_workspace_size",
+    "gale_route_select", "gale_mx4_layout", "gale_mx8_layout", "gale_mx4_quantize", "gale_mx4_unpack",
+    "gale_mx8_quantize", "gale_mx_gemm_workspace_size", "gale_mx_gemm", "gale_rmsnorm",
 )
 
 GALE_NOALLOC_SCRATCH_BYTES = 4 << 20
@@ -61,6 +64,12 @@ class gale_w4_layout_t(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("q_offset", ctypes.c_int64),
                 ("q_bytes", ctypes.c_int64), ("s_offset", ctypes.c_int64), ("s_bytes", ctypes.c_int64),
                 ("total", ctypes.c_int64)]
+
+
+class gale_mx_layout_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("cols_padded", ctypes.c_int64),
+                ("q_offset", ctypes.c_int64), ("q_bytes", ctypes.c_int64), ("s_offset", ctypes.c_int64),
+                ("s_bytes", ctypes.c_int64), ("total", ctypes.c_int64)]
 
 
 class gale_layer(ctypes.Structure):
@@ -113,6 +122,17 @@ def lib() -> ctypes.CDLL:
             "gale_w4_quantize": (i32, [vp, i64, i64, vp, vp]),
             "gale_w4_workspace_size": (sz, [i64, i64, i32]),
             "gale_w4_gemv": (i32, [vp, i64, i64, vp, i32, vp, vp, sz, vp]),
+            "gale_route_select": (i32, [vp, i32, i64, vp, i32, i32, i32, i32, i32, i32, i32, i32, ctypes.c_float, vp,
+                                        vp, vp]),
+            "gale_mx4_layout": (i32, [i64, i64, ctypes.POINTER(gale_mx_layout_t)]),
+            "gale_mx8_layout": (i32, [i64, i64, ctypes.POINTER(gale_mx_layout_t)]),
+            "gale_mx4_quantize": (i32, [vp, i32, i64, i64, i64, vp, vp]),
+            "gale_mx4_unpack": (i32, [vp, i64, i64, vp, i32, i64, vp]),
+            "gale_mx8_quantize": (i32, [vp, i32, i64, i64, i64, vp, vp]),
+            "gale_mx_gemm_workspace_size": (sz, [i64, i64, i64]),
+            "gale_mx_gemm": (i32, [vp, i64, i64, vp, i64, vp, i32, i64, vp, sz, vp]),
+            "gale_rmsnorm": (i32, [vp, vp, i32, i64, i64, vp, i32, ctypes.c_float, i64, i64, vp, i64, vp, i32, i64,
+                                   vp, vp]),
             "gale_selftest_scratch_bytes": (sz, []),
             "gale_selftest": (i32, [vp, vp]),
         }
@@ -272,6 +292,105 @@ def gale_w4_gemv(packed, rows: int, cols: int, x, y, ws, stream=None):
     B = x.shape[0]
     _check(lib().gale_w4_gemv(_ptr(packed), rows, cols, _ptr(x), B, _ptr(y), _ptr(ws), ws.numel() * ws.element_size(),
                               _stream(stream)), "gale_w4_gemv")
+
+
+def _rows2(t, where: str):
+    """Row stride in elements of a [rows, cols] tensor whose rows are contiguous."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise GaleError(GALE_ERR_ARG, where + " (rows must be contiguous)")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _mx_room(packed, rows: int, cols: int, mx4: bool, where: str):
+    """Refuse a packed buffer that is smaller than its layout."""
+    rp, cp = (rows + 127) // 128 * 128, (cols + 127) // 128 * 128
+    q = rp * cp // 2 if mx4 else rows * cp
+    if packed.numel() * packed.element_size() < (q + 255) // 256 * 256 + rp * cp // 32:
+        raise GaleError(GALE_ERR_ARG, where + " (packed buffer smaller than its layout)")
+
+
+def gale_route_select(logits, ids, gates, bias=None, score: int = GALE_SCORE_SOFTMAX, n_groups: int = 1,
+                      keep_groups: int = 1, group_top: int = 1, renorm: bool = True, scale: float = 1.0, stream=None):
+    """Top-K experts (K = ids.shape[1]) of every token by score, selection bias and groups, and their gates."""
+    B, E = logits.shape
+    if ids.shape != gates.shape or ids.shape[0] != B or not (ids.is_contiguous() and gates.is_contiguous()):
+        raise GaleError(GALE_ERR_ARG, "gale_route_select (ids and gates are contiguous [B, K])")
+    if bias is not None and (bias.shape != (E,) or not bias.is_contiguous()):
+        raise GaleError(GALE_ERR_ARG, "gale_route_select (bias is [E])")
+    _check(lib().gale_route_select(_ptr(logits), _dtype_code(logits), _rows2(logits, "gale_route_select"), _ptr(bias),
+                                   B, E, ids.shape[1], score, n_groups, keep_groups, group_top, bool(renorm), scale,
+                                   _ptr(ids), _ptr(gates), _stream(stream)), "gale_route_select")
+
+
+def gale_mx4_layout(rows: int, cols: int) -> gale_mx_layout_t:
+    out = gale_mx_layout_t()
+    _check(lib().gale_mx4_layout(rows, cols, ctypes.byref(out)), "gale_mx4_layout")
+    return out
+
+
+def gale_mx8_layout(tokens: int, cols: int) -> gale_mx_layout_t:
+    out = gale_mx_layout_t()
+    _check(lib().gale_mx8_layout(tokens, cols, ctypes.byref(out)), "gale_mx8_layout")
+    return out
+
+
+def gale_mx4_quantize(w, packed, stream=None):
+    """Quantize a device [rows, cols] matrix to MXFP4 (packed: device bytes of gale_mx4_layout)."""
+    rows, cols = w.shape
+    _mx_room(packed, rows, cols, True, "gale_mx4_quantize")
+    _check(lib().gale_mx4_quantize(_ptr(w), _dtype_code(w), _rows2(w, "gale_mx4_quantize"), rows, cols, _ptr(packed),
+                                   _stream(stream)), "gale_mx4_quantize")
+
+
+def gale_mx4_unpack(packed, out, stream=None):
+    """out [rows, cols] = the values a packed MXFP4 matrix stands for."""
+    rows, cols = out.shape
+    _mx_room(packed, rows, cols, True, "gale_mx4_unpack")
+    _check(lib().gale_mx4_unpack(_ptr(packed), rows, cols, _ptr(out), _dtype_code(out),
+                                 _rows2(out, "gale_mx4_unpack"), _stream(stream)), "gale_mx4_unpack")
+
+
+def gale_mx8_quantize(x, packed, stream=None):
+    """Quantize device tokens [tokens, cols] to MXFP8 (packed: device bytes of gale_mx8_layout)."""
+    tokens, cols = x.shape
+    _mx_room(packed, tokens, cols, False, "gale_mx8_quantize")
+    _check(lib().gale_mx8_quantize(_ptr(x), _dtype_code(x), _rows2(x, "gale_mx8_quantize"), tokens, cols, _ptr(packed),
+                                   _stream(stream)), "gale_mx8_quantize")
+
+
+def gale_mx_gemm_workspace_size(rows: int, cols: int, tokens: int) -> int:
+    return int(lib().gale_mx_gemm_workspace_size(rows, cols, tokens))
+
+
+def gale_mx_gemm(w4, rows: int, cols: int, x8, y, ws, stream=None):
+    """y [tokens, rows] = the MXFP8 tokens x8 times the MXFP4 matrix w4 [rows, cols] transposed."""
+    if y.dim() != 2 or y.shape[1] != rows:
+        raise GaleError(GALE_ERR_ARG, "gale_mx_gemm (y is [tokens, rows])")
+    _mx_room(w4, rows, cols, True, "gale_mx_gemm")
+    _mx_room(x8, y.shape[0], cols, False, "gale_mx_gemm")
+    _check(lib().gale_mx_gemm(_ptr(w4), rows, cols, _ptr(x8), y.shape[0], _ptr(y), _dtype_code(y),
+                              _rows2(y, "gale_mx_gemm"), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "gale_mx_gemm")
+
+
+def gale_rmsnorm(x, y=None, residual=None, weight=None, sum_out=None, mx8=None, eps: float = 1e-6, stream=None):
+    """h = x + residual; y = h / sqrt(mean h^2 + eps) * weight, as y and / or MXFP8 bytes; sum_out = h."""
+    tokens, cols = x.shape
+    w = "gale_rmsnorm"
+    for t in (residual, sum_out):
+        if t is not None and (t.dtype != x.dtype or t.shape != x.shape):
+            raise GaleError(GALE_ERR_ARG, w + " (residual and sum_out have x's shape and type)")
+    if y is not None and y.shape != x.shape:
+        raise GaleError(GALE_ERR_ARG, w + " (y has x's shape)")
+    if weight is not None and (weight.shape != (cols,) or not weight.is_contiguous()):
+        raise GaleError(GALE_ERR_ARG, w + " (weight is [cols])")
+    if mx8 is not None:
+        _mx_room(mx8, tokens, cols, False, w)
+    _check(lib().gale_rmsnorm(
+        _ptr(x), _ptr(residual), _dtype_code(x), _rows2(x, w), 0 if residual is None else _rows2(residual, w),
+        _ptr(weight), 0 if weight is None else _dtype_code(weight), eps, tokens, cols, _ptr(sum_out),
+        0 if sum_out is None else _rows2(sum_out, w), _ptr(y), 0 if y is None else _dtype_code(y),
+        0 if y is None else _rows2(y, w), _ptr(mx8), _stream(stream)), w)
 
 
 def make_layer(base, expert_stride: int, n_experts: int, d_model: int, d_ff: int) -> gale_layer:

@@ -54,6 +54,10 @@ extern "C" {
 #define GALE_MODE_PLAIN  0        /* y = Q(W) x_rot */
 #define GALE_MODE_SWIGLU 1        /* y = silu(Q(W) x_rot) * (Q(W3) x_rot) */
 
+/* gale_route_select scores */
+#define GALE_SCORE_SOFTMAX 0      /* s = exp(l - max l) / sum exp(l - max l) over all experts */
+#define GALE_SCORE_SIGMOID 1      /* s = 1 / (1 + exp(-l)) */
+
 /* gale_moe_forward flags */
 #define GALE_FLAG_RESIDUAL_RMSNORM 1  /* out = bf16(RMSNorm(x + y)), unit weight */
 
@@ -193,6 +197,42 @@ int gale_route_permute_grid(const int32_t* ids, int B, int K, int E, int32_t* co
  * Errors: GALE_ERR_ARG (sizes, NULL pointers), GALE_ERR_ALIGN.
  * ------------------------------------------------------------------------- */
 int gale_route_topk(const float* logits, int B, int E, int K, int32_t* ids, float* gates, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Router by scores: an interface addition for routers that score with a
+ * sigmoid or a softmax, choose with a bias that balances the experts' load,
+ * limit the choice to the best groups of experts, and renormalise the gates.
+ * Per token, from its E logits:
+ *   s_e    = the score (GALE_SCORE_SOFTMAX or GALE_SCORE_SIGMOID)
+ *   key_e  = s_e + bias[e]; without a bias the logit itself (the score grows
+ *            with it)
+ *   groups : n_groups groups of E / n_groups consecutive experts; a group's
+ *            score is the sum of its group_top (1 or 2) largest s_e + bias[e];
+ *            the keep_groups best groups stay (the lower group first on equal
+ *            scores).  n_groups = 1 leaves them out.
+ *   picks  : the K largest keys of the experts that stay, by descending key;
+ *            the lower expert index first on equal keys
+ *   gates  : scale * s_e, or with renorm scale * s_e / (sum of the picks' s);
+ *            the bias never enters a gate
+ * A logit of -inf (or NaN) masks its expert: its score is 0, its key -inf, and
+ * it adds nothing to its group's score (a group of masked experts has -inf).  Every
+ * finite logit is scored, the type's lowest too; +inf counts as the largest
+ * finite fp32.  Where too few experts are left, masked ones are picked with
+ * gate 0; a token whose picks' scores are all 0 has gates 0.  A NaN s_e + bias
+ * counts as -inf.  The order is that of the 64-bit values of these formulas;
+ * gates are fp32.
+ *   logits : device [B][E] of logits_dtype (GALE_F32, GALE_BF16, GALE_F16),
+ *            rows ld elements apart (ld >= E)
+ *   bias   : device fp32 [E], or NULL
+ *   ids    : device int32 [B][K];   gates : device fp32 [B][K]
+ * 1 <= K <= 16, K <= E <= 1024, 1 <= n_groups <= 32 dividing E,
+ * 1 <= keep_groups <= n_groups with keep_groups * (E / n_groups) >= K, B >= 0
+ * (0 is a no-op).  One launch, one warp per token; the outputs feed
+ * gale_moe_forward directly.  Errors: GALE_ERR_ARG, GALE_ERR_ALIGN.
+ * ------------------------------------------------------------------------- */
+int gale_route_select(const void* logits, int logits_dtype, int64_t ld, const float* bias, int B, int E,
+                      int K, int score, int n_groups, int keep_groups, int group_top, int renorm,
+                      float scale, int32_t* ids, float* gates, void* stream);
 
 /* ---------------------------------------------------------------------------
  * One routed-expert MoE layer.
@@ -443,6 +483,100 @@ size_t gale_w4_workspace_size(int64_t rows, int64_t cols, int B);   /* host only
                                                                         unsupported sizes */
 int gale_w4_gemv(const void* packed, int64_t rows, int64_t cols, const uint16_t* x, int B, float* y, void* ws,
                  size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Microscaled weights and tokens (an interface addition: a 4-bit form of the
+ * non-expert weights whose products run on the tensor cores for any number of
+ * tokens).  32 consecutive columns of a row share a scale 2^k, stored as one
+ * byte k + 127; 255 stands for a block that held an infinity or a NaN, and its
+ * values are NaN.  Codes are e2m1 (MXFP4: 0, .5, 1, 1.5, 2, 3, 4, 6 and a sign)
+ * or e4m3 (MXFP8, largest 448); a value is code * 2^k.  Reading: k is the
+ * smallest exponent with max|v| <= 2^k * (largest code), clamped to
+ * [-127, 127] (-127 for a block of zeros), so that no value is clipped; codes
+ * are v / 2^k rounded to nearest even.  Every decision is exact in fp32.
+ *
+ * MXFP4 matrix [rows x cols] (gale_mx4_layout), tiles of 128 x 128, padding
+ * zero:
+ *   q at q_offset = 0 : [ceil(rows/128)][ceil(cols/128)][128][64] bytes; column
+ *                       c of a tile's row in byte c/2, the low nibble even c
+ *   s at s_offset     : [ceil(rows/128)][ceil(cols/128)][512] bytes; the scale
+ *                       of (row r, block b of the tile) is byte
+ *                       (r % 32) * 16 + (r / 32) * 4 + b
+ * MXFP8 tokens [tokens x cols] (gale_mx8_layout): q [tokens][cols_padded]
+ * bytes (columns past cols zero), s as above with rows = tokens (the scales of
+ * rows past the last token are never written nor used).
+ * Sections and totals are 256-byte aligned.  1 <= rows <= 2^24,
+ * 1 <= cols <= 2^20, and (padded rows / 128) * padded cols < 2^31.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int64_t rows, cols, cols_padded;
+    int64_t q_offset, q_bytes;
+    int64_t s_offset, s_bytes;
+    int64_t total;
+} gale_mx_layout_t;
+
+/* Host only.  Errors: GALE_ERR_ARG (NULL out, sizes). */
+int gale_mx4_layout(int64_t rows, int64_t cols, gale_mx_layout_t* out);
+int gale_mx8_layout(int64_t tokens, int64_t cols, gale_mx_layout_t* out);
+
+/* A dense matrix to MXFP4.
+ *   w      : device [rows][cols] of w_dtype, rows ld elements apart (ld >= cols)
+ *   packed : device, gale_mx4_layout(...).total bytes, 256-byte aligned, codes
+ *            and scales fully written
+ * One launch; 16-byte aligned rows are read fastest.  Errors: GALE_ERR_ARG,
+ * GALE_ERR_ALIGN. */
+int gale_mx4_quantize(const void* w, int w_dtype, int64_t ld, int64_t rows, int64_t cols, void* packed,
+                      void* stream);
+
+/* The values an MXFP4 matrix stands for, rounded once to out_dtype, into out
+ * [rows][cols], rows ld elements apart.  Errors: GALE_ERR_ARG, GALE_ERR_ALIGN. */
+int gale_mx4_unpack(const void* packed, int64_t rows, int64_t cols, void* out, int out_dtype, int64_t ld,
+                    void* stream);
+
+/* Tokens x [tokens][cols] of x_dtype, rows ld elements apart, to MXFP8 (packed:
+ * gale_mx8_layout(...).total bytes, 256-byte aligned).  tokens == 0 is a no-op.
+ * Errors: GALE_ERR_ARG, GALE_ERR_ALIGN. */
+int gale_mx8_quantize(const void* x, int x_dtype, int64_t ld, int64_t tokens, int64_t cols, void* packed,
+                      void* stream);
+
+/* y[t][r] = sum_c W[r][c] X[t][c], W an MXFP4 matrix [rows x cols], X MXFP8
+ * tokens [tokens x cols]; sums in fp32, rounded once to y_dtype.
+ *   y  : device [tokens][rows] of y_dtype, rows ldy elements apart (ldy >= rows)
+ *   ws : device, 256-byte aligned, gale_mx_gemm_workspace_size() bytes; its
+ *        first int32 is a sticky status word: the caller sets it to 0 once, the
+ *        call never clears it and writes GALE_ERR_TIMEOUT there if a bounded
+ *        wait inside the kernel ran out (results are then undefined)
+ * Any token count (0 is a no-op).  The sums' order depends on the sizes alone:
+ * equal calls give equal bits.
+ * Errors: GALE_ERR_ARG, GALE_ERR_ALIGN, GALE_ERR_WORKSPACE, GALE_ERR_CUDA. */
+size_t gale_mx_gemm_workspace_size(int64_t rows, int64_t cols, int64_t tokens);   /* host only; 0 on invalid sizes */
+int gale_mx_gemm(const void* w4, int64_t rows, int64_t cols, const void* x8, int64_t tokens, void* y,
+                 int y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * RMSNorm with the residual's addition (an interface addition: the norm between
+ * sublayers, which GALE_FLAG_RESIDUAL_RMSNORM has only fused behind the
+ * experts, with unit weight).  Per token, in fp32:
+ *   h = x + residual (h = x without one)
+ *   y = h / sqrt(mean_c h^2 + eps) * weight
+ * h enters the norm before its own rounding.
+ *   x, residual : device [tokens][cols] of dtype, rows ldx / ldr elements apart;
+ *                 residual may be NULL
+ *   weight      : device [cols] of w_dtype, or NULL (1)
+ *   sum_out     : device [tokens][cols] of dtype (h, rounded), or NULL; may be x
+ *                 or residual themselves (same address and stride)
+ *   y           : device [tokens][cols] of y_dtype, or NULL; may be x or
+ *                 residual themselves where the types are equal
+ *   mx8         : MXFP8 tokens of y before its rounding to y_dtype
+ *                 (gale_mx8_layout(tokens, cols), 256-byte aligned), or NULL
+ * At least one output.  1 <= cols <= 32768 (GALE_ERR_UNSUPPORTED beyond),
+ * 0 <= tokens < 2^31, eps >= 0.  16-byte aligned rows run fastest.  The sum of
+ * squares is taken in fp32: rows with |h| above about 1e19 overflow it.
+ * Errors: GALE_ERR_ARG, GALE_ERR_ALIGN, GALE_ERR_UNSUPPORTED, GALE_ERR_CUDA.
+ * ------------------------------------------------------------------------- */
+int gale_rmsnorm(const void* x, const void* residual, int dtype, int64_t ldx, int64_t ldr,
+                 const void* weight, int w_dtype, float eps, int64_t tokens, int64_t cols, void* sum_out,
+                 int64_t ldsum, void* y, int y_dtype, int64_t ldy, void* mx8, void* stream);
 
 /* Built-in parity self-check on tiny shapes (the card's "optional fast paths
  * verify themselves at startup" -- without any fallback).  Synchronous:
