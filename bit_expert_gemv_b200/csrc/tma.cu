@@ -37,6 +37,37 @@ int make_map_3d(CUtensorMap* m, bool u16, const void* base, uint64_t d0, uint64_
     return r == CUDA_SUCCESS ? GALE_OK : GALE_ERR_CUDA;
 }
 
+// Packed MXFP4 tiles as lines of 128 nibbles (64 bytes), boxes of 128 lines (a
+// 128 x 128 tile): every 16 nibbles land in the first half of a 16-byte chunk
+// (the second half is padding), 128-byte swizzle.
+int make_map_mx4(CUtensorMap* m, const void* base, int64_t lines) {
+    auto fn = encode_fn();
+    if (!fn) return GALE_ERR_CUDA;
+    cuuint64_t dims[2] = {128, cuuint64_t(lines)};
+    cuuint64_t strides[1] = {64};
+    cuuint32_t box[2] = {128, 128};
+    cuuint32_t es[2] = {1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void*>(base), dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GALE_OK : GALE_ERR_CUDA;
+}
+
+// A [rows][pitch] byte matrix, boxes of box_cols x box_rows, 128-byte swizzle;
+// rows past the last read as zero.
+int make_map_bytes(CUtensorMap* m, const void* base, int64_t pitch, int64_t rows, int box_cols, int box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return GALE_ERR_CUDA;
+    cuuint64_t dims[2] = {cuuint64_t(pitch), cuuint64_t(rows)};
+    cuuint64_t strides[1] = {cuuint64_t(pitch)};
+    cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)};
+    cuuint32_t es[2] = {1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GALE_OK : GALE_ERR_CUDA;
+}
+
 // Sign words of one matrix kind across experts: [experts][rows][cols/32] uint32,
 // boxes of 32 words (1024 columns) x 16 rows, 128-byte swizzle.
 int make_sign_map(CUtensorMap* m, const void* first_matrix, int rows, int cols, int experts, int64_t stride) {
