@@ -161,18 +161,32 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _stream(stream):
+_torch = None
+_codes = None       # torch dtype -> dtype code
+
+
+def _load_torch():
+    global _torch, _codes
     import torch
+    _codes = {torch.float32: GALE_F32, torch.bfloat16: GALE_BF16, torch.float16: GALE_F16}
+    _torch = torch
+    return torch
+
+
+def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle, without building a Stream object (3 us) on every call
+        c = (_torch or _load_torch())._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
 def _dtype_code(t) -> int:
-    import torch
-    return {torch.float32: GALE_F32, torch.bfloat16: GALE_BF16, torch.float16: GALE_F16}[t.dtype]
+    if _codes is None:
+        _load_torch()
+    return _codes[t.dtype]
 
 
 # ----------------------------------------------------------------------------
@@ -294,32 +308,36 @@ def gale_w4_gemv(packed, rows: int, cols: int, x, y, ws, stream=None):
                               _stream(stream)), "gale_w4_gemv")
 
 
-def _rows2(t, where: str):
-    """Row stride in elements of a [rows, cols] tensor whose rows are contiguous."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+def _rows2(t, shape, where: str):
+    """Row stride in elements of a [rows, cols] tensor of this shape whose rows are contiguous."""
+    if t.shape != shape:
+        raise GaleError(GALE_ERR_ARG, where + " (a tensor of another shape)")
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
         raise GaleError(GALE_ERR_ARG, where + " (rows must be contiguous)")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return ld if ld >= shape[1] or shape[0] > 1 else shape[1]
 
 
 def _mx_room(packed, rows: int, cols: int, mx4: bool, where: str):
     """Refuse a packed buffer that is smaller than its layout."""
     rp, cp = (rows + 127) // 128 * 128, (cols + 127) // 128 * 128
     q = rp * cp // 2 if mx4 else rows * cp
-    if packed.numel() * packed.element_size() < (q + 255) // 256 * 256 + rp * cp // 32:
+    if packed.nbytes < (q + 255) // 256 * 256 + rp * cp // 32:
         raise GaleError(GALE_ERR_ARG, where + " (packed buffer smaller than its layout)")
 
 
 def gale_route_select(logits, ids, gates, bias=None, score: int = GALE_SCORE_SOFTMAX, n_groups: int = 1,
                       keep_groups: int = 1, group_top: int = 1, renorm: bool = True, scale: float = 1.0, stream=None):
     """Top-K experts (K = ids.shape[1]) of every token by score, selection bias and groups, and their gates."""
-    B, E = logits.shape
-    if ids.shape != gates.shape or ids.shape[0] != B or not (ids.is_contiguous() and gates.is_contiguous()):
+    shape, picks = logits.shape, ids.shape
+    B, E = shape
+    if picks != gates.shape or len(picks) != 2 or picks[0] != B or not (ids.is_contiguous() and gates.is_contiguous()):
         raise GaleError(GALE_ERR_ARG, "gale_route_select (ids and gates are contiguous [B, K])")
     if bias is not None and (bias.shape != (E,) or not bias.is_contiguous()):
         raise GaleError(GALE_ERR_ARG, "gale_route_select (bias is [E])")
-    _check(lib().gale_route_select(_ptr(logits), _dtype_code(logits), _rows2(logits, "gale_route_select"), _ptr(bias),
-                                   B, E, ids.shape[1], score, n_groups, keep_groups, group_top, bool(renorm), scale,
-                                   _ptr(ids), _ptr(gates), _stream(stream)), "gale_route_select")
+    _check(lib().gale_route_select(logits.data_ptr(), _dtype_code(logits), _rows2(logits, shape, "gale_route_select"),
+                                   _ptr(bias), B, E, picks[1], score, n_groups, keep_groups, group_top, 1 if renorm else 0,
+                                   scale, ids.data_ptr(), gates.data_ptr(), _stream(stream)), "gale_route_select")
 
 
 def gale_mx4_layout(rows: int, cols: int) -> gale_mx_layout_t:
@@ -338,7 +356,7 @@ def gale_mx4_quantize(w, packed, stream=None):
     """Quantize a device [rows, cols] matrix to MXFP4 (packed: device bytes of gale_mx4_layout)."""
     rows, cols = w.shape
     _mx_room(packed, rows, cols, True, "gale_mx4_quantize")
-    _check(lib().gale_mx4_quantize(_ptr(w), _dtype_code(w), _rows2(w, "gale_mx4_quantize"), rows, cols, _ptr(packed),
+    _check(lib().gale_mx4_quantize(_ptr(w), _dtype_code(w), _rows2(w, w.shape, "gale_mx4_quantize"), rows, cols, _ptr(packed),
                                    _stream(stream)), "gale_mx4_quantize")
 
 
@@ -347,14 +365,14 @@ def gale_mx4_unpack(packed, out, stream=None):
     rows, cols = out.shape
     _mx_room(packed, rows, cols, True, "gale_mx4_unpack")
     _check(lib().gale_mx4_unpack(_ptr(packed), rows, cols, _ptr(out), _dtype_code(out),
-                                 _rows2(out, "gale_mx4_unpack"), _stream(stream)), "gale_mx4_unpack")
+                                 _rows2(out, out.shape, "gale_mx4_unpack"), _stream(stream)), "gale_mx4_unpack")
 
 
 def gale_mx8_quantize(x, packed, stream=None):
     """Quantize device tokens [tokens, cols] to MXFP8 (packed: device bytes of gale_mx8_layout)."""
     tokens, cols = x.shape
     _mx_room(packed, tokens, cols, False, "gale_mx8_quantize")
-    _check(lib().gale_mx8_quantize(_ptr(x), _dtype_code(x), _rows2(x, "gale_mx8_quantize"), tokens, cols, _ptr(packed),
+    _check(lib().gale_mx8_quantize(_ptr(x), _dtype_code(x), _rows2(x, x.shape, "gale_mx8_quantize"), tokens, cols, _ptr(packed),
                                    _stream(stream)), "gale_mx8_quantize")
 
 
@@ -364,33 +382,42 @@ def gale_mx_gemm_workspace_size(rows: int, cols: int, tokens: int) -> int:
 
 def gale_mx_gemm(w4, rows: int, cols: int, x8, y, ws, stream=None):
     """y [tokens, rows] = the MXFP8 tokens x8 times the MXFP4 matrix w4 [rows, cols] transposed."""
-    if y.dim() != 2 or y.shape[1] != rows:
+    shape = y.shape
+    if len(shape) != 2 or shape[1] != rows:
         raise GaleError(GALE_ERR_ARG, "gale_mx_gemm (y is [tokens, rows])")
     _mx_room(w4, rows, cols, True, "gale_mx_gemm")
-    _mx_room(x8, y.shape[0], cols, False, "gale_mx_gemm")
-    _check(lib().gale_mx_gemm(_ptr(w4), rows, cols, _ptr(x8), y.shape[0], _ptr(y), _dtype_code(y),
-                              _rows2(y, "gale_mx_gemm"), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+    _mx_room(x8, shape[0], cols, False, "gale_mx_gemm")
+    _check(lib().gale_mx_gemm(w4.data_ptr(), rows, cols, x8.data_ptr(), shape[0], y.data_ptr(), _dtype_code(y),
+                              _rows2(y, shape, "gale_mx_gemm"), ws.data_ptr(), ws.nbytes, _stream(stream)),
            "gale_mx_gemm")
 
 
 def gale_rmsnorm(x, y=None, residual=None, weight=None, sum_out=None, mx8=None, eps: float = 1e-6, stream=None):
     """h = x + residual; y = h / sqrt(mean h^2 + eps) * weight, as y and / or MXFP8 bytes; sum_out = h."""
-    tokens, cols = x.shape
-    w = "gale_rmsnorm"
-    for t in (residual, sum_out):
-        if t is not None and (t.dtype != x.dtype or t.shape != x.shape):
-            raise GaleError(GALE_ERR_ARG, w + " (residual and sum_out have x's shape and type)")
-    if y is not None and y.shape != x.shape:
-        raise GaleError(GALE_ERR_ARG, w + " (y has x's shape)")
-    if weight is not None and (weight.shape != (cols,) or not weight.is_contiguous()):
-        raise GaleError(GALE_ERR_ARG, w + " (weight is [cols])")
+    where = "gale_rmsnorm"
+    shape = x.shape
+    tokens, cols = shape
+    dt = x.dtype
+    r = h = out = w = 0
+    ldr = ldh = ldy = wt = yt = 0
+    if residual is not None:
+        r, ldr = residual.data_ptr(), _rows2(residual, shape, where)
+        if residual.dtype != dt:
+            raise GaleError(GALE_ERR_ARG, where + " (residual has x's type)")
+    if sum_out is not None:
+        h, ldh = sum_out.data_ptr(), _rows2(sum_out, shape, where)
+        if sum_out.dtype != dt:
+            raise GaleError(GALE_ERR_ARG, where + " (sum_out has x's type)")
+    if y is not None:
+        out, ldy, yt = y.data_ptr(), _rows2(y, shape, where), _dtype_code(y)
+    if weight is not None:
+        if weight.shape != (cols,) or not weight.is_contiguous():
+            raise GaleError(GALE_ERR_ARG, where + " (weight is [cols])")
+        w, wt = weight.data_ptr(), _dtype_code(weight)
     if mx8 is not None:
-        _mx_room(mx8, tokens, cols, False, w)
-    _check(lib().gale_rmsnorm(
-        _ptr(x), _ptr(residual), _dtype_code(x), _rows2(x, w), 0 if residual is None else _rows2(residual, w),
-        _ptr(weight), 0 if weight is None else _dtype_code(weight), eps, tokens, cols, _ptr(sum_out),
-        0 if sum_out is None else _rows2(sum_out, w), _ptr(y), 0 if y is None else _dtype_code(y),
-        0 if y is None else _rows2(y, w), _ptr(mx8), _stream(stream)), w)
+        _mx_room(mx8, tokens, cols, False, where)
+    _check(lib().gale_rmsnorm(x.data_ptr(), r, _dtype_code(x), _rows2(x, shape, where), ldr, w, wt, eps, tokens, cols, h,
+                              ldh, out, yt, ldy, _ptr(mx8), _stream(stream)), where)
 
 
 def make_layer(base, expert_stride: int, n_experts: int, d_model: int, d_ff: int) -> gale_layer:

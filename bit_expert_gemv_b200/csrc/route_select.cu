@@ -27,6 +27,8 @@ struct SelectArgs {
     int dtype, sigmoid, renorm;
     int groups, gsize, keep, gtop;
     float scale;
+    int lanes_log2;         // 2^lanes_log2 lanes read a group's keys: as many as 32 / groups allows
+    uint32_t gmagic;        // ceil(2^20 / gsize): e / gsize = e * gmagic >> 20 for e < 1024
 };
 
 constexpr float kMinusInf = -INFINITY;
@@ -200,19 +202,188 @@ __device__ __forceinline__ void write_picks(const SelectArgs& a, int64_t t, int 
     }
 }
 
+// Unsigned order of a float: larger value, larger integer (-0 as +0); 0 is below every value's.
+__device__ __forceinline__ uint32_t order_bits(float f) {
+    const uint32_t u = __float_as_uint(f + 0.0f);
+    return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t o) {
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+
+// A lane's two largest keys that are not taken, the lower place first on equal keys.
+template <int V>
+__device__ __forceinline__ void lane_top2(const uint32_t (&key)[V], uint32_t taken, uint32_t& h1, int& j1, uint32_t& h2,
+                                          int& j2) {
+    h1 = h2 = 0u;
+    j1 = j2 = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const uint32_t k = (taken >> j) & 1u ? 0u : key[j];
+        const bool first = k > h1, second = k > h2;
+        h2 = first ? h1 : second ? k : h2;
+        j2 = first ? j1 : second ? j : j2;
+        h1 = first ? k : h1;
+        j1 = first ? j : j1;
+    }
+}
+
+// Picks 0 .. n - 1 by descending key, the lower expert first on equal keys: lane
+// k returns pick k's expert and its key (0: there were no more).  Every round
+// takes the largest of the lanes' heads; a lane that gives its head moves its
+// second up, and looks through its keys again only when it gives a third.
+template <int V>
+__device__ __forceinline__ int take_largest(const uint32_t (&key)[V], int n, int lane, uint32_t& my_key) {
+    uint32_t taken = 0u, h1, h2;
+    int j1, j2, mine = 0;
+    bool have2 = true;
+    lane_top2<V>(key, taken, h1, j1, h2, j2);
+    my_key = 0u;
+    for (int k = 0; k < n; ++k) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, h1);
+        const int e = lane + 32 * j1;
+        const int id = int(__reduce_min_sync(0xffffffffu, h1 == m ? uint32_t(e) : 0xFFFFu));
+        if (lane == k) {
+            mine = id;
+            my_key = m;
+        }
+        if (e == id && h1 == m) {
+            taken |= 1u << j1;
+            if (have2) {
+                h1 = h2;
+                j1 = j2;
+                have2 = false;
+            } else {
+                lane_top2<V>(key, taken, h1, j1, h2, j2);
+                have2 = true;
+            }
+        }
+    }
+    return mine;
+}
+
+// Whether a >= b is certain to be the order of the 64-bit values when either
+// is known to es + 2^-24 |value|.  Infinities are exact.
+__device__ __forceinline__ bool certain(float a, float b, float es) {
+    return a - b > 2.0f * es + 2.4e-7f * fmaxf(fabsf(a), fabsf(b)) || (a == b && isinf(a)) || b == kMinusInf;
+}
+
 template <int V>
 __global__ void __launch_bounds__(256) route_select_kernel(SelectArgs a) {
+    __shared__ float group_keys[8][33 * V];
     const int lane = threadIdx.x & 31;
-    const int64_t t = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int64_t t = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
     if (t >= a.B) return;
-    const int id = select_exact<V>(a, t, lane);
-    float lmax = kMinusInf, sum = 0.f;
-    if (!a.sigmoid && !a.renorm) {
-        for (int e = lane; e < a.E; e += 32) lmax = fmaxf(lmax, logit_at(a, t, e));
-        lmax = fmaxf(warp_max_t(lmax), -kFltMax);
-        for (int e = lane; e < a.E; e += 32) sum += expf(logit_at(a, t, e) - lmax);
-        sum = warp_sum(sum);
+    float l[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int e = lane + 32 * j;
+        l[j] = e < a.E ? logit_at(a, t, e) : kMinusInf;
     }
+    float lmax = kMinusInf, sum = 0.f;
+    uint32_t key[V];
+    bool sure = true;
+    const bool scored = a.bias || a.groups > 1;
+    if (!scored) {
+        // no bias, no groups: the keys are the logits
+#pragma unroll
+        for (int j = 0; j < V; ++j) key[j] = lane + 32 * j < a.E ? order_bits(l[j]) : 0u;
+        if (!a.sigmoid && !a.renorm) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) lmax = fmaxf(lmax, l[j]);
+            lmax = fmaxf(warp_max_t(lmax), -kFltMax);
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum += __expf(l[j] - lmax);
+            sum = warp_sum(sum);
+        }
+    } else {
+        // fp32 scores and what they may be off by
+        float s[V], es;
+        if (a.sigmoid) {
+            // exp to 2^-22 relatively, 1 + exp and the quotient to two units: below 2^-21 of 1
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] = __fdividef(1.0f, 1.0f + __expf(-l[j]));
+            es = 4.8e-7f;
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) lmax = fmaxf(lmax, l[j]);
+            lmax = fmaxf(warp_max_t(lmax), -kFltMax);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                s[j] = __expf(l[j] - lmax);
+                sum += s[j];
+            }
+            sum = warp_sum(sum);
+            const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] *= inv;
+            // the largest score is inv; V + 5 additions, the exponentials (whose argument's rounding
+            // times the exponential stays below half a unit of 1), the quotient
+            es = inv * float(V + 24) * 1.2e-7f;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int e = lane + 32 * j;
+            s[j] = with_bias(s[j], a.bias && e < a.E ? __ldg(a.bias + e) : 0.f, l[j] == kMinusInf);
+        }
+        uint32_t kept = 0xFFFFFFFFu;
+        if (a.groups > 1 && a.keep < a.groups) {
+            // a group's keys to L neighbouring lanes through shared memory (a pad word per 32 against bank conflicts)
+            float* gk = group_keys[threadIdx.x >> 5];
+#pragma unroll
+            for (int j = 0; j < V; ++j) gk[lane + 33 * j] = s[j];
+            __syncwarp();
+            const int lg = a.lanes_log2, L = 1 << lg;
+            const int g = lane >> lg;
+            float m1 = kMinusInf, m2 = kMinusInf;
+            if (g < a.groups) {
+                for (int i = lane & (L - 1); i < a.gsize; i += L) {
+                    const int e = g * a.gsize + i;
+                    const float v = gk[e + (e >> 5)];
+                    m2 = fmaxf(m2, fminf(m1, v));
+                    m1 = fmaxf(m1, v);
+                }
+            }
+            for (int o = 1; o < L; o <<= 1) {
+                const float u1 = __shfl_xor_sync(0xffffffffu, m1, o), u2 = __shfl_xor_sync(0xffffffffu, m2, o);
+                m2 = fmaxf(fmaxf(m2, u2), fminf(m1, u1));
+                m1 = fmaxf(m1, u1);
+            }
+            float score = a.gtop == 2 && m2 > kMinusInf ? m1 + m2 : m1;
+            if (!(score == score)) score = kMinusInf;
+            score = __shfl_sync(0xffffffffu, score, (lane << lg) & 31);
+            if (lane >= a.groups) score = kMinusInf;
+            // what a sum of two is off by: twice es, and the roundings of the keys and of the sum
+            const float mag = fmaxf(fabsf(m1), m2 > kMinusInf ? fabsf(m2) : 0.f);
+            const float big = warp_max_t(g < a.groups && mag < INFINITY ? mag : 0.f);
+            kept = kept_groups(a, score, lane);
+            const bool in = (kept >> lane) & 1u;
+            const float worst = -warp_max_t(in ? -score : kMinusInf);
+            const float best = warp_max_t(lane < a.groups && !in ? score : kMinusInf);
+            sure = certain(worst, best, 2.0f * es + 4.8e-7f * big);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int e = lane + 32 * j;
+            const int g = a.groups > 1 ? int(uint32_t(e) * a.gmagic >> 20) : 0;
+            const bool live = e < a.E && ((kept >> g) & 1u);
+            key[j] = live ? order_bits(a.bias ? s[j] : l[j]) : 0u;
+        }
+        if (a.bias && sure) {
+            // one more than is picked: the last pick's lead counts too
+            uint32_t mk;
+            const int id = take_largest<V>(key, a.K + 1, lane, mk);
+            const uint32_t nk = __shfl_down_sync(0xffffffffu, mk, 1);
+            const bool clear = lane >= a.K || nk == 0u || certain(order_value(mk), order_value(nk), es);
+            if (__all_sync(0xffffffffu, clear)) {
+                write_picks(a, t, lane, id, lmax, sum);
+                return;
+            }
+            sure = false;
+        }
+    }
+    uint32_t mk;
+    const int id = sure ? take_largest<V>(key, a.K, lane, mk) : select_exact<V>(a, t, lane);
     write_picks(a, t, lane, id, lmax, sum);
 }
 
@@ -235,7 +406,10 @@ extern "C" int gale_route_select(const void* logits, int logits_dtype, int64_t l
     if (!aligned(logits, logits_dtype == GALE_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(gates, 4))
         return GALE_ERR_ALIGN;
     SelectArgs a{logits, bias, ids, gates, ld, B, E, K, logits_dtype, score == GALE_SCORE_SIGMOID, renorm != 0,
-                 n_groups, gsize, keep_groups, group_top, scale};
+                 n_groups, gsize, keep_groups, group_top, scale, 0, 0u};
+    while ((2 << a.lanes_log2) * n_groups <= 32) ++a.lanes_log2;
+    // exact quotients: e * (gmagic * gsize - 2^20) < 2^20 for e < 1024, gsize <= 1024
+    a.gmagic = ((1u << 20) + gsize - 1) / gsize;
     cudaStream_t st = as_stream(stream);
     const unsigned grid = unsigned((B + 7) / 8);
     if (E <= 32) route_select_kernel<1><<<grid, 256, 0, st>>>(a);
