@@ -9,9 +9,12 @@
 //   gate  = scale * s (/ sum of the picks' s)
 //
 // A warp per token; lane l holds experts l, l + 32, ...  The order is that of
-// the 64-bit values of these formulas.  It is taken in fp32 first: every value
-// is known to within `err`, and a comparison that the error could turn is
-// settled by computing the candidates again in 64 bits (select_exact).
+// the 64-bit values of these formulas.  It is taken in fp32 first, where every
+// value is known to within a bound; a comparison that the bound leaves open is
+// settled with the candidates' 64-bit values (refine), and where more than a
+// few are in question the whole token is done in 64 bits (select_exact).
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace gale {
@@ -36,11 +39,31 @@ constexpr float kFltMax = 3.402823466e38f;
 
 // The logit as the formulas take it: NaN counts as -inf, +inf as the largest finite number.
 __device__ __forceinline__ float clean(float l) {
-    l = l == l ? l : kMinusInf;
-    return l > kFltMax ? kFltMax : l;
+    return fminf(fmaxf(l, kMinusInf), kFltMax);      // fmaxf drops a NaN
 }
 __device__ __forceinline__ float logit_at(const SelectArgs& a, int64_t t, int e) {
     return clean(load_as_f32(a.logits, a.dtype, t * a.ld + e));
+}
+// The logits of experts lane, lane + 32, ...; -inf past the last.
+template <int V>
+__device__ __forceinline__ void load_logits(const SelectArgs& a, int64_t t, int lane, float (&l)[V]) {
+    if (a.dtype == GALE_F32) {
+        const float* p = static_cast<const float*>(a.logits) + t * a.ld + lane;
+#pragma unroll
+        for (int j = 0; j < V; ++j) l[j] = lane + 32 * j < a.E ? __ldg(p + 32 * j) : kMinusInf;
+    } else {
+        const uint16_t* p = static_cast<const uint16_t*>(a.logits) + t * a.ld + lane;
+        uint16_t u[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) u[j] = lane + 32 * j < a.E ? __ldg(p + 32 * j) : 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float f = a.dtype == GALE_BF16 ? bf16_to_f32(u[j]) : __half2float(__ushort_as_half(u[j]));
+            l[j] = lane + 32 * j < a.E ? f : kMinusInf;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) l[j] = clean(l[j]);
 }
 // s + b, -inf for a masked expert or a NaN
 template <typename T>
@@ -65,33 +88,42 @@ __device__ __forceinline__ T warp_sum_t(T v) {
     return v;
 }
 
-// Group scores by warp-wide passes over the groups: lane g returns group g's.
-template <typename T, int V>
-__device__ __forceinline__ T group_scores(const SelectArgs& a, const T (&sel)[V], int lane) {
-    T mine = T(-INFINITY);
-    for (int g = 0; g < a.groups; ++g) {
-        const int lo = g * a.gsize, hi = lo + a.gsize;
-        T m1 = T(-INFINITY), m2 = T(-INFINITY);
+// Group scores in 64 bits by warp-wide passes over the groups, four at a time
+// (their shuffles overlap): lane g returns group g's.
+template <int V>
+__device__ __forceinline__ double group_scores(const SelectArgs& a, const double (&sel)[V], int lane) {
+    double mine = -INFINITY;
+    for (int g0 = 0; g0 < a.groups; g0 += 4) {
+        double m1[4], m2[4];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int e = lane + 32 * j;
-            if (e >= lo && e < hi) {
-                const T v = sel[j];
-                if (v > m1) { m2 = m1; m1 = v; }
-                else if (v > m2) m2 = v;
+        for (int q = 0; q < 4; ++q) {
+            const int lo = (g0 + q) * a.gsize, hi = lo + a.gsize;
+            m1[q] = m2[q] = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int e = lane + 32 * j;
+                const double v = e >= lo && e < hi && e < a.E ? sel[j] : -INFINITY;
+                const double low = m1[q] > v ? v : m1[q];
+                m1[q] = m1[q] > v ? m1[q] : v;
+                m2[q] = m2[q] > low ? m2[q] : low;
             }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const T u1 = __shfl_xor_sync(0xffffffffu, m1, o), u2 = __shfl_xor_sync(0xffffffffu, m2, o);
-            const T low = m1 > u1 ? u1 : m1;             // the smaller of the two maxima
-            m1 = m1 > u1 ? m1 : u1;
-            m2 = m2 > u2 ? m2 : u2;
-            m2 = m2 > low ? m2 : low;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const double u1 = __shfl_xor_sync(0xffffffffu, m1[q], o), u2 = __shfl_xor_sync(0xffffffffu, m2[q], o);
+                const double low = m1[q] > u1 ? u1 : m1[q];             // the smaller of the two maxima
+                m1[q] = m1[q] > u1 ? m1[q] : u1;
+                m2[q] = m2[q] > u2 ? m2[q] : u2;
+                m2[q] = m2[q] > low ? m2[q] : low;
+            }
         }
-        T score = m1;
-        if (a.gtop == 2 && m2 > T(-INFINITY)) score = m1 + m2;
-        if (lane == g) mine = score == score ? score : T(-INFINITY);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const double score = a.gtop == 2 && m2[q] > -INFINITY ? m1[q] + m2[q] : m1[q];
+            if (lane == g0 + q) mine = score == score ? score : -INFINITY;
+        }
     }
     return mine;
 }
@@ -112,13 +144,10 @@ template <int V>
 __device__ __noinline__ int select_exact(const SelectArgs& a, int64_t t, int lane) {
     double sel[V];
     float l[V];
+    load_logits<V>(a, t, lane, l);
     float lmax = kMinusInf;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int e = lane + 32 * j;
-        l[j] = e < a.E ? logit_at(a, t, e) : kMinusInf;
-        lmax = fmaxf(lmax, l[j]);
-    }
+    for (int j = 0; j < V; ++j) lmax = fmaxf(lmax, l[j]);
     lmax = fmaxf(warp_max_t(lmax), -kFltMax);
     double sum = 0.0;
 #pragma unroll
@@ -134,7 +163,7 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, int64_t t, int lan
         sel[j] = with_bias(sel[j], a.bias && e < a.E ? a.bias[e] : 0.f, l[j] == kMinusInf);
     }
     uint32_t kept = 0xFFFFFFFFu;
-    if (a.groups > 1) kept = kept_groups(a, group_scores<double, V>(a, sel, lane), lane);
+    if (a.groups > 1) kept = kept_groups(a, group_scores<V>(a, sel, lane), lane);
     uint32_t out = 0u;     // bit j: expert lane + 32 j does not exist, is taken, or its group went
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -169,39 +198,6 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, int64_t t, int lan
     return mine;
 }
 
-// Gates of the picks (lane k holds pick k), written with the ids.  `lmax` and
-// `sum`: the softmax's maximum and denominator, read where they are needed.
-__device__ __forceinline__ void write_picks(const SelectArgs& a, int64_t t, int lane, int id, float lmax, float sum) {
-    const bool on = lane < a.K;
-    const float l = on ? logit_at(a, t, id) : kMinusInf;
-    float g;
-    if (a.sigmoid) {
-        const float s = 1.0f / (1.0f + expf(-l));
-        g = s;
-        if (a.renorm) {
-            const float z = warp_sum(s);
-            g = z > 0.f ? s / z : 0.f;
-            if (z < 1e-30f) {       // scores at the end of fp32's range: their ratios in 64 bits
-                const double d = l == kMinusInf ? 0.0 : 1.0 / (1.0 + exp(-double(l)));
-                const double zd = warp_sum_t(d);
-                g = zd > 0.0 ? float(d / zd) : 0.f;
-            }
-        }
-    } else if (a.renorm) {
-        // relative to the largest pick: the softmax's denominator cancels
-        const float m = fmaxf(warp_max_t(l), -kFltMax);
-        const float s = expf(l - m);
-        const float z = warp_sum(s);
-        g = z > 0.f ? s / z : 0.f;
-    } else {
-        g = sum > 0.f ? expf(l - lmax) / sum : 0.f;
-    }
-    if (on) {
-        a.ids[t * a.K + lane] = id;
-        a.gates[t * a.K + lane] = g * a.scale;
-    }
-}
-
 // Unsigned order of a float: larger value, larger integer (-0 as +0); 0 is below every value's.
 __device__ __forceinline__ uint32_t order_bits(float f) {
     const uint32_t u = __float_as_uint(f + 0.0f);
@@ -209,6 +205,130 @@ __device__ __forceinline__ uint32_t order_bits(float f) {
 }
 __device__ __forceinline__ float order_value(uint32_t o) {
     return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+
+// Whether a >= b is certain to be the order of the 64-bit values when either
+// is known to es + 2^-24 |value|.  Infinities are exact.
+__device__ __forceinline__ bool certain(float a, float b, float es) {
+    return a - b > 2.0f * es + 2.4e-7f * fmaxf(fabsf(a), fabsf(b)) || (a == b && isinf(a)) || b == kMinusInf;
+}
+
+// The denominator of the softmax in 64 bits.
+template <int V>
+__device__ __forceinline__ double softmax_sum64(const float (&l)[V], float lmax) {
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum += exp(double(l[j]) - double(lmax));
+    return warp_sum_t(sum);
+}
+// The score of one logit in fp32 (to within the caller's `es`) and in 64 bits.
+__device__ __forceinline__ float score32(const SelectArgs& a, float l, float lmax, float inv) {
+    return a.sigmoid ? __frcp_rn(1.0f + expf(-l)) : __expf(l - lmax) * inv;
+}
+__device__ __forceinline__ double score64(const SelectArgs& a, float l, float lmax, double sum) {
+    return a.sigmoid ? 1.0 / (1.0 + exp(-double(l))) : sum > 0.0 ? exp(double(l) - double(lmax)) / sum : 0.0;
+}
+
+// Sorts n <= 32 candidates (one per lane, `live`) by descending key, the lower
+// id first: lane r gets the r-th.
+template <typename T>
+__device__ __forceinline__ void sort_lanes(int n, int lane, bool live, T& key, int& id) {
+    int rank = live ? 0 : 32;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const T o = __shfl_sync(0xffffffffu, key, i);
+        const int oid = __shfl_sync(0xffffffffu, live ? id : -1, i);
+        rank += oid >= 0 && (o > key || (o == key && oid < id));
+    }
+    const T k0 = key;
+    const int id0 = id;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const int r = __shfl_sync(0xffffffffu, rank, i), oid = __shfl_sync(0xffffffffu, id0, i);
+        const T o = __shfl_sync(0xffffffffu, k0, i);
+        if (r == lane) {
+            key = o;
+            id = oid;
+        }
+    }
+}
+
+// Picks with a bias where the packed keys leave their order in doubt: lane i
+// holds the i-th largest of n packed keys, `m` (0: there were no more).  Sorts
+// them by their fp32 keys, and by the 64-bit ones if those are in doubt too.
+// False if an expert that is not among them could still belong to the picks.
+template <int V>
+__device__ __noinline__ bool refine(const SelectArgs& a, int64_t t, int lane, int n, float es, float lmax, float inv,
+                                    uint32_t m, int& id) {
+    constexpr uint32_t kIndex = 32 * V - 1;
+    const bool live = lane < n && m != 0u;
+    const int count = __popc(__ballot_sync(0xffffffffu, live));
+    const uint32_t last = __shfl_sync(0xffffffffu, m, n - 1);
+    const int first = live ? int(kIndex - (m & kIndex)) : 0;
+    const float l = live ? logit_at(a, t, first) : kMinusInf;
+    const float b = live ? a.bias[first] : 0.f;
+    float key = with_bias(score32(a, l, lmax, inv), b, l == kMinusInf);
+    id = first;
+    sort_lanes(n, lane, live, key, id);
+    const float next = __shfl_down_sync(0xffffffffu, key, 1);
+    if (__any_sync(0xffffffffu, lane < a.K && lane + 1 < count && !certain(key, next, es))) {
+        double sum = 1.0;
+        if (!a.sigmoid) {
+            float all[V];
+            load_logits<V>(a, t, lane, all);
+            sum = softmax_sum64<V>(all, lmax);
+        }
+        double exact = with_bias(score64(a, l, lmax, sum), b, l == kMinusInf);
+        id = first;
+        sort_lanes(n, lane, live, exact, id);
+        key = float(exact);
+    }
+    const float kth = __shfl_sync(0xffffffffu, key, a.K - 1);
+    return last == 0u || certain(kth, order_value(last | kIndex), es);
+}
+
+// The sum over lanes 0 .. K - 1 (zeros from K on), valid in those lanes.
+template <typename T>
+__device__ __forceinline__ T picks_sum(int K, T v) {
+    for (int o = 1; o < K; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Gates of the picks (lane k holds pick k), written with the ids.  `lmax` and
+// `sum`: the softmax's maximum and denominator, read where they are needed.
+__device__ __forceinline__ void write_picks(const SelectArgs& a, int64_t t, int lane, int id, float lmax, float sum) {
+    const bool on = lane < a.K;
+    const float l = on ? logit_at(a, t, id) : kMinusInf;
+    float g, z;
+    if (a.sigmoid) {
+        g = __fdividef(1.0f, 1.0f + __expf(-l));      // 0 past the last pick
+        if (a.renorm) {
+            z = picks_sum(a.K, g);
+            if (__any_sync(0xffffffffu, on && z < 1e-30f)) {
+                // scores at the end of fp32's range: their ratios in 64 bits
+                const double d = l == kMinusInf ? 0.0 : 1.0 / (1.0 + exp(-double(l)));
+                const double zd = picks_sum(a.K, d);
+                g = zd > 0.0 ? float(d / zd) : 0.f;
+            } else {
+                g = __fdividef(g, z);
+            }
+        }
+    } else if (a.renorm) {
+        // relative to the largest pick: the softmax's denominator cancels
+        float m = l;
+        if (a.bias) m = warp_max_t(l);
+        else m = __shfl_sync(0xffffffffu, l, 0);
+        g = __expf(l - fmaxf(m, -kFltMax));
+        z = picks_sum(a.K, g);
+        g = z > 0.f ? __fdividef(g, z) : 0.f;
+    } else {
+        g = sum > 0.f ? __fdividef(__expf(l - lmax), sum) : 0.f;
+    }
+    if (on) {
+        const int64_t at = t * a.K + lane;
+        a.ids[at] = id;
+        a.gates[at] = g * a.scale;
+    }
 }
 
 // A lane's two largest keys that are not taken, the lower place first on equal keys.
@@ -229,24 +349,22 @@ __device__ __forceinline__ void lane_top2(const uint32_t (&key)[V], uint32_t tak
 }
 
 // Picks 0 .. n - 1 by descending key, the lower expert first on equal keys: lane
-// k returns pick k's expert and its key (0: there were no more).  Every round
-// takes the largest of the lanes' heads; a lane that gives its head moves its
+// k returns pick k's expert.  Every round takes the largest of the lanes' heads; a lane that gives its head moves its
 // second up, and looks through its keys again only when it gives a third.
 template <int V>
-__device__ __forceinline__ int take_largest(const uint32_t (&key)[V], int n, int lane, uint32_t& my_key) {
+__device__ __forceinline__ int take_largest(const uint32_t (&key)[V], int n, int lane) {
     uint32_t taken = 0u, h1, h2;
     int j1, j2, mine = 0;
     bool have2 = true;
     lane_top2<V>(key, taken, h1, j1, h2, j2);
-    my_key = 0u;
     for (int k = 0; k < n; ++k) {
         const uint32_t m = __reduce_max_sync(0xffffffffu, h1);
         const int e = lane + 32 * j1;
-        const int id = int(__reduce_min_sync(0xffffffffu, h1 == m ? uint32_t(e) : 0xFFFFu));
-        if (lane == k) {
-            mine = id;
-            my_key = m;
-        }
+        const uint32_t who = __ballot_sync(0xffffffffu, h1 == m);
+        int id;
+        if ((who & (who - 1)) == 0) id = __shfl_sync(0xffffffffu, e, __ffs(who) - 1);
+        else id = int(__reduce_min_sync(0xffffffffu, h1 == m ? uint32_t(e) : 0xFFFFu));   // equal keys
+        if (lane == k) mine = id;
         if (e == id && h1 == m) {
             taken |= 1u << j1;
             if (have2) {
@@ -262,73 +380,138 @@ __device__ __forceinline__ int take_largest(const uint32_t (&key)[V], int n, int
     return mine;
 }
 
-// Whether a >= b is certain to be the order of the 64-bit values when either
-// is known to es + 2^-24 |value|.  Infinities are exact.
-__device__ __forceinline__ bool certain(float a, float b, float es) {
-    return a - b > 2.0f * es + 2.4e-7f * fmaxf(fabsf(a), fabsf(b)) || (a == b && isinf(a)) || b == kMinusInf;
+// A lane's three largest packed keys below `under`.
+template <int V>
+__device__ __forceinline__ void lane_top3(const uint32_t (&pk)[V], uint32_t under, uint32_t& h1, uint32_t& h2,
+                                          uint32_t& h3) {
+    h1 = h2 = h3 = 0u;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        uint32_t k = pk[j] < under ? pk[j] : 0u, low = min(h1, k);
+        h1 = max(h1, k);
+        k = min(h2, low);
+        h2 = max(h2, low);
+        h3 = max(h3, k);
+    }
 }
 
+// The same picks from packed keys: the leading bits of a key's order over the
+// expert's index (inverted: the lower one first), so that one warp-wide maximum
+// a round gives both.  Keys of 16-bit logits fit whole; others may tie here,
+// which the caller sees from neighbouring picks.  Lane k returns pick k (0:
+// none).  A lane that has given its third key looks for its next three.
 template <int V>
-__global__ void __launch_bounds__(256) route_select_kernel(SelectArgs a) {
-    __shared__ float group_keys[8][33 * V];
+__device__ __forceinline__ uint32_t take_packed(const uint32_t (&pk)[V], int n, int lane) {
+    uint32_t h1, h2, h3, mine = 0u;
+    lane_top3<V>(pk, 0xFFFFFFFFu, h1, h2, h3);
+    for (int k = 0; k < n; ++k) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, h1);
+        mine = lane == k ? m : mine;
+        const bool own = h1 == m;
+        h1 = own ? h2 : h1;
+        h2 = own ? h3 : h2;
+        h3 = own ? 0u : h3;
+        if (V > 3 && __any_sync(0xffffffffu, own && h1 == 0u)) {
+            uint32_t g1, g2, g3;
+            lane_top3<V>(pk, m, g1, g2, g3);
+            if (own) {
+                h1 = g1;
+                h2 = g2;
+                h3 = g3;
+            }
+        }
+    }
+    return mine;
+}
+
+// CTAs of 8 warps that an SM is to hold.
+template <int V, bool SCORED>
+constexpr int select_ctas() {
+    return V <= 8 ? (SCORED ? 3 : 5) : V == 16 ? (SCORED ? 2 : 3) : (SCORED ? 1 : 2);
+}
+
+// SCORED: with a bias or groups; otherwise the keys are the logits.
+template <int V, bool SCORED>
+__global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_kernel(const __grid_constant__ SelectArgs a) {
+    __shared__ float group_keys[SCORED ? 8 : 1][SCORED ? 33 * V : 1];
+    constexpr uint32_t kIndex = 32 * V - 1;      // the bits of a packed key that hold the expert
     const int lane = threadIdx.x & 31;
     const int64_t t = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
     if (t >= a.B) return;
     float l[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int e = lane + 32 * j;
-        l[j] = e < a.E ? logit_at(a, t, e) : kMinusInf;
-    }
+    load_logits<V>(a, t, lane, l);
     float lmax = kMinusInf, sum = 0.f;
-    uint32_t key[V];
-    bool sure = true;
-    const bool scored = a.bias || a.groups > 1;
-    if (!scored) {
-        // no bias, no groups: the keys are the logits
+    uint32_t pk[V];
+    int id = 0;
+    if (!a.sigmoid && (SCORED || !a.renorm)) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) key[j] = lane + 32 * j < a.E ? order_bits(l[j]) : 0u;
+        for (int j = 0; j < V; ++j) lmax = fmaxf(lmax, l[j]);
+        lmax = fmaxf(warp_max_t(lmax), -kFltMax);
+    }
+    if constexpr (!SCORED) {
         if (!a.sigmoid && !a.renorm) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) lmax = fmaxf(lmax, l[j]);
-            lmax = fmaxf(warp_max_t(lmax), -kFltMax);
 #pragma unroll
             for (int j = 0; j < V; ++j) sum += __expf(l[j] - lmax);
             sum = warp_sum(sum);
         }
-    } else {
-        // fp32 scores and what they may be off by
-        float s[V], es;
-        if (a.sigmoid) {
-            // exp to 2^-22 relatively, 1 + exp and the quotient to two units: below 2^-21 of 1
-#pragma unroll
-            for (int j = 0; j < V; ++j) s[j] = __fdividef(1.0f, 1.0f + __expf(-l[j]));
-            es = 4.8e-7f;
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) lmax = fmaxf(lmax, l[j]);
-            lmax = fmaxf(warp_max_t(lmax), -kFltMax);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                s[j] = __expf(l[j] - lmax);
-                sum += s[j];
-            }
-            sum = warp_sum(sum);
-            const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) s[j] *= inv;
-            // the largest score is inv; V + 5 additions, the exponentials (whose argument's rounding
-            // times the exponential stays below half a unit of 1), the quotient
-            es = inv * float(V + 24) * 1.2e-7f;
-        }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int e = lane + 32 * j;
-            s[j] = with_bias(s[j], a.bias && e < a.E ? __ldg(a.bias + e) : 0.f, l[j] == kMinusInf);
+            pk[j] = e < a.E ? (order_bits(l[j]) & ~kIndex) | (kIndex - e) : 0u;
+        }
+        // 16-bit logits are packed whole; others with one more than is picked, to see a tie of the last
+        const bool whole = a.dtype != GALE_F32;
+        const uint32_t m = take_packed<V>(pk, whole ? a.K : a.K + 1, lane);
+        id = int(kIndex - (m & kIndex));
+        if (!whole) {
+            const uint32_t next = __shfl_down_sync(0xffffffffu, m, 1);
+            if (__any_sync(0xffffffffu, lane < a.K && next != 0u && ((m ^ next) & ~kIndex) == 0u)) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) pk[j] = lane + 32 * j < a.E ? order_bits(l[j]) : 0u;
+                id = take_largest<V>(pk, a.K, lane);
+            }
+        }
+    } else {
+        // fp32 scores are needed of every expert with a bias, else of the groups' best;
+        // es: what one may be off by
+        float inv = 0.f, es;
+        if (a.sigmoid) {
+            // exp good to a unit in the last place (s (1 - s) 2^-23 <= 2^-25 in s), the
+            // rounding of 1 + exp (2^-24 s) and of the reciprocal (2^-25): 2^-23.  A faster
+            // exponential and quotient would quadruple that and the tokens taken in 64 bits.
+            es = 1.2e-7f;
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum += __expf(l[j] - lmax);
+            sum = warp_sum(sum);
+            inv = sum > 0.f ? 1.0f / sum : 0.f;
+            // the largest score is inv; V + 5 additions, the exponentials (whose argument's
+            // rounding times the exponential stays below half a unit of 1), the quotient
+            es = inv * float(V + 24) * 1.2e-7f;
+        }
+        float s[V];         // keys in fp32
+        if (!a.bias) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[j] = l[j];
+        } else {
+            if (a.sigmoid) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) s[j] = __frcp_rn(1.0f + expf(-l[j]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) s[j] = __expf(l[j] - lmax) * inv;
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int e = lane + 32 * j;
+                s[j] = with_bias(s[j], e < a.E ? __ldg(a.bias + e) : 0.f, l[j] == kMinusInf);
+            }
         }
         uint32_t kept = 0xFFFFFFFFu;
+        bool sure = true;
         if (a.groups > 1 && a.keep < a.groups) {
-            // a group's keys to L neighbouring lanes through shared memory (a pad word per 32 against bank conflicts)
+            // a group's keys to 2^lanes_log2 neighbouring lanes through shared memory (a pad word per 32
+            // against bank conflicts), its two largest to lane g
             float* gk = group_keys[threadIdx.x >> 5];
 #pragma unroll
             for (int j = 0; j < V; ++j) gk[lane + 33 * j] = s[j];
@@ -349,41 +532,59 @@ __global__ void __launch_bounds__(256) route_select_kernel(SelectArgs a) {
                 m2 = fmaxf(fmaxf(m2, u2), fminf(m1, u1));
                 m1 = fmaxf(m1, u1);
             }
-            float score = a.gtop == 2 && m2 > kMinusInf ? m1 + m2 : m1;
-            if (!(score == score)) score = kMinusInf;
-            score = __shfl_sync(0xffffffffu, score, (lane << lg) & 31);
-            if (lane >= a.groups) score = kMinusInf;
+            m1 = __shfl_sync(0xffffffffu, m1, (lane << lg) & 31);
+            m2 = __shfl_sync(0xffffffffu, m2, (lane << lg) & 31);
+            if (lane >= a.groups) m1 = m2 = kMinusInf;
+            if (a.gtop == 1) m2 = kMinusInf;
             // what a sum of two is off by: twice es, and the roundings of the keys and of the sum
-            const float mag = fmaxf(fabsf(m1), m2 > kMinusInf ? fabsf(m2) : 0.f);
-            const float big = warp_max_t(g < a.groups && mag < INFINITY ? mag : 0.f);
+            const float k1 = a.bias || m1 == kMinusInf ? m1 : score32(a, m1, lmax, inv);
+            const float k2 = a.bias || m2 == kMinusInf ? m2 : score32(a, m2, lmax, inv);
+            const float f1 = fabsf(k1), f2 = fabsf(k2);
+            const float big = warp_max_t(fmaxf(f1 < INFINITY ? f1 : 0.f, f2 < INFINITY ? f2 : 0.f));
+            float score = k2 > kMinusInf ? k1 + k2 : k1;
+            if (!(score == score)) score = kMinusInf;
             kept = kept_groups(a, score, lane);
             const bool in = (kept >> lane) & 1u;
             const float worst = -warp_max_t(in ? -score : kMinusInf);
             const float best = warp_max_t(lane < a.groups && !in ? score : kMinusInf);
             sure = certain(worst, best, 2.0f * es + 4.8e-7f * big);
+            if (!sure && !a.bias) {
+                // the best two of a group are certain (by logit): their scores in 64 bits
+                const double all = a.sigmoid ? 1.0 : softmax_sum64<V>(l, lmax);
+                const double d1 = score64(a, m1, lmax, all), d2 = score64(a, m2, lmax, all);
+                kept = kept_groups(a, m1 == kMinusInf ? double(kMinusInf) : m2 == kMinusInf ? d1 : d1 + d2, lane);
+                sure = true;
+            }
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
+            // an expert whose group went: 0, below every key
             const int e = lane + 32 * j;
             const int g = a.groups > 1 ? int(uint32_t(e) * a.gmagic >> 20) : 0;
-            const bool live = e < a.E && ((kept >> g) & 1u);
-            key[j] = live ? order_bits(a.bias ? s[j] : l[j]) : 0u;
+            pk[j] = e < a.E && ((kept >> g) & 1u) ? (order_bits(s[j]) & ~kIndex) | (kIndex - e) : 0u;
         }
-        if (a.bias && sure) {
+        if (sure) {
             // one more than is picked: the last pick's lead counts too
-            uint32_t mk;
-            const int id = take_largest<V>(key, a.K + 1, lane, mk);
-            const uint32_t nk = __shfl_down_sync(0xffffffffu, mk, 1);
-            const bool clear = lane >= a.K || nk == 0u || certain(order_value(mk), order_value(nk), es);
-            if (__all_sync(0xffffffffu, clear)) {
-                write_picks(a, t, lane, id, lmax, sum);
-                return;
+            const uint32_t m = take_packed<V>(pk, a.K + 1, lane);
+            const uint32_t next = __shfl_down_sync(0xffffffffu, m, 1);
+            id = int(kIndex - (m & kIndex));
+            if (a.bias) {
+                // m's key is at least, next's at most
+                const float low = order_value(m & ~kIndex), high = order_value(next | kIndex);
+                if (!__all_sync(0xffffffffu, lane >= a.K || next == 0u || certain(low, high, es))) {
+                    const int n = a.K + 8;
+                    const uint32_t mn = take_packed<V>(pk, n, lane);
+                    sure = refine<V>(a, t, lane, n, es, lmax, inv, mn, id);
+                }
+            } else if (a.dtype == GALE_F32 &&
+                       __any_sync(0xffffffffu, lane < a.K && next != 0u && ((m ^ next) & ~kIndex) == 0u)) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) pk[j] = pk[j] != 0u ? order_bits(l[j]) : 0u;
+                id = take_largest<V>(pk, a.K, lane);
             }
-            sure = false;
         }
+        if (!sure) id = select_exact<V>(a, t, lane);
     }
-    uint32_t mk;
-    const int id = sure ? take_largest<V>(key, a.K, lane, mk) : select_exact<V>(a, t, lane);
     write_picks(a, t, lane, id, lmax, sum);
 }
 
@@ -412,12 +613,17 @@ extern "C" int gale_route_select(const void* logits, int logits_dtype, int64_t l
     a.gmagic = ((1u << 20) + gsize - 1) / gsize;
     cudaStream_t st = as_stream(stream);
     const unsigned grid = unsigned((B + 7) / 8);
-    if (E <= 32) route_select_kernel<1><<<grid, 256, 0, st>>>(a);
-    else if (E <= 64) route_select_kernel<2><<<grid, 256, 0, st>>>(a);
-    else if (E <= 128) route_select_kernel<4><<<grid, 256, 0, st>>>(a);
-    else if (E <= 256) route_select_kernel<8><<<grid, 256, 0, st>>>(a);
-    else if (E <= 512) route_select_kernel<16><<<grid, 256, 0, st>>>(a);
-    else route_select_kernel<32><<<grid, 256, 0, st>>>(a);
+    auto launch = [&](auto v) {
+        constexpr int V = decltype(v)::value;
+        if (a.bias || a.groups > 1) route_select_kernel<V, true><<<grid, 256, 0, st>>>(a);
+        else route_select_kernel<V, false><<<grid, 256, 0, st>>>(a);
+    };
+    if (E <= 32) launch(std::integral_constant<int, 1>());
+    else if (E <= 64) launch(std::integral_constant<int, 2>());
+    else if (E <= 128) launch(std::integral_constant<int, 4>());
+    else if (E <= 256) launch(std::integral_constant<int, 8>());
+    else if (E <= 512) launch(std::integral_constant<int, 16>());
+    else launch(std::integral_constant<int, 32>());
     GALE_LAUNCH_CHECK();
     return GALE_OK;
 }
