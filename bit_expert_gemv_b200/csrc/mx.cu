@@ -123,9 +123,9 @@ __global__ void __launch_bounds__(256) mx8_quantize_kernel(const void* __restric
 constexpr int64_t kMxMaxRows = int64_t(1) << 24, kMxMaxCols = int64_t(1) << 20;
 
 bool mx_sizes(int64_t rows, int64_t cols) {
-    // the tile index (rows / 128 * cols / 128) and its 128 tensor-map rows stay below 2^31
+    // the tensor-map rows of all tiles stay well below 2^31
     return rows >= 1 && rows <= kMxMaxRows && cols >= 1 && cols <= kMxMaxCols &&
-           align_up(rows, kMxTile) / kMxTile * align_up(cols, kMxTile) < (int64_t(1) << 31);
+           align_up(rows, kMxTile) / kMxTile * align_up(cols, kMxTile) < (int64_t(1) << 30);
 }
 
 }  // namespace

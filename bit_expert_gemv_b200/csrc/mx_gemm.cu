@@ -8,11 +8,22 @@
 // arithmetic instruction touches a weight: a few tokens are bound by the
 // weights' stream from HBM, many by the tensor pipe.
 //
-// Roles (192 threads): warp 0 fills a ring of stages (128 columns each) by TMA;
-// one lane of warp 1 copies the stage's scales to TMEM and issues its four
-// MMAs; warps 2-5 read the accumulators and write y.  Where there are fewer
-// tiles than SMs, a cluster of 2 to 8 CTAs splits the columns of one tile and
-// adds the partial sums through distributed shared memory, in rank order.
+// The kernel is persistent, one CTA per SM.  Roles (256 threads): warps 0 and 2
+// fill a ring of stages (256 columns each) with weights and with tokens; a lane
+// of warp 1 copies a stage's scales to TMEM and issues its eight MMAs; warps
+// 4-7 read a tile's accumulators and write y while the next tile's MMAs run
+// into the other accumulator buffer.  What a few instructions of one lane cost
+// sets the pace of the rings: a turn of a producer's loop takes some 400 cycles
+// (waiting for a stage, the copies' issue), which 128 columns of a stage did not
+// cover.
+//
+// PAIR: two CTAs share a tile of 256 rows.  Either holds its own 128 rows and
+// half of the tokens' bytes, so a CTA's shared memory takes in 24 KB instead of
+// 40 KB per 128 x 128 x 256 products; the first CTA issues for both.
+//
+// Without PAIR, the tiles that are left after whole rounds are split over the
+// columns by a cluster of up to 8 CTAs, whose partial sums are added through
+// distributed shared memory in rank order.
 #include "mx.cuh"
 #include "tc_mx.cuh"
 #include "tma.cuh"
@@ -20,10 +31,11 @@
 namespace gale {
 namespace {
 
-constexpr int kGThreads = 192;
-constexpr int kGABytes = kMxTile * kMxTile;      // a stage's weights: 128 rows x 128 columns, a byte each
+constexpr int kGThreads = 256;
+constexpr int kGK = 2;                           // column tiles of a stage
+constexpr int kGABytes = kMxTile * kMxTile;      // weights of a column tile: 128 rows x 128 columns, a byte each
 constexpr int kGMaxStages = 8;
-constexpr int kGSfCols = 16;                     // TMEM columns of a stage's scales: 4 (W) + up to 12 (X)
+constexpr int kGMaxShared = 96;                  // columns that the two accumulator buffers may share
 constexpr int kGMaxN = 256;
 constexpr int kGSmemSm = 226 * 1024;             // dynamic shared memory a CTA can have (1 KB for the barriers)
 
@@ -34,190 +46,498 @@ struct GemmArgs {
     int32_t* status;
     int64_t rows, tokens, ldy;
     int nt;                 // column tiles
+    int rtiles;             // 128-row tiles
     int n;                  // tokens of a tile (the MMA's N)
     int ntt;                // token tiles
+    int tiles;              // row tiles (of 256 rows with PAIR) x token tiles
     int xatoms;             // scale atoms a token tile can touch
-    int split;              // CTAs per tile (the cluster)
+    int sfcols;             // TMEM columns of a stage's scales: per column tile 4 (W) and 4 per atom (X)
+    int workers;            // CTAs (pairs with PAIR) that take whole tiles
+    int whole;              // tiles that each worker takes whole (the last one may be missing when split is 1)
+    int split;              // CTAs that share a left-over tile (the cluster)
+    int joint;              // left-over tiles of a cluster, at most
     int stages;
     int stage_bytes;
     int cols;               // TMEM columns
+    int d1;                 // TMEM column of the second accumulator buffer
     int ydtype;
+    int pair16;             // 16-bit y may be written two rows at a time
 };
 
-__global__ void __launch_bounds__(kGThreads) mx_gemm_kernel(const __grid_constant__ CUtensorMap wmap,
-                                                           const __grid_constant__ CUtensorMap xmap, GemmArgs a) {
+// Unit u of this CTA: a tile and a range of its column tiles.
+struct GemmUnit {
+    int rt, tt, k0, k1;
+    bool joint;
+};
+template <bool PAIR>
+__device__ __forceinline__ bool gemm_unit(const GemmArgs& a, int u, GemmUnit& w) {
+    const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+    int tile;
+    if (u < a.whole) {
+        tile = u * a.workers + worker;
+        w.k0 = 0;
+        w.k1 = a.nt;
+        w.joint = false;
+    } else {
+        if (PAIR || u >= a.whole + a.joint) return false;
+        const int cluster = blockIdx.x / a.split, part = blockIdx.x % a.split;
+        tile = a.whole * a.workers + cluster + (u - a.whole) * (a.workers / a.split);
+        const int pieces = (a.nt + kGK - 1) / kGK;
+        w.k0 = pieces * part / a.split * kGK;
+        w.k1 = min(pieces * (part + 1) / a.split * kGK, a.nt);
+        w.joint = true;
+    }
+    if (tile >= a.tiles) return false;
+    w.rt = tile / a.ntt;
+    w.tt = tile % a.ntt;
+    return true;
+}
+
+// 16 tokens of one row per lane to y; `full`: all of the warp's rows exist.
+__device__ __forceinline__ void gemm_store16(const GemmArgs& a, int64_t t, int64_t row, int lane, bool full,
+                                             const float (&v)[16]) {
+    if (a.ydtype == GALE_F32) {
+        float* y = static_cast<float*>(a.y) + t * a.ldy + row;
+        if (full && t + 16 <= a.tokens) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                *y = v[i];
+                y += a.ldy;
+            }
+        } else if (row < a.rows) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (t + i < a.tokens) *y = v[i];
+                y += a.ldy;
+            }
+        }
+    } else if (a.pair16) {
+        // lanes 2i and 2i + 1 trade values so that each writes two rows of one of two tokens
+        const int odd = lane & 1;
+        const int64_t r0 = row - odd;
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+            w[i / 2] = pack16(a.ydtype, odd ? got : v[i], odd ? v[i + 1] : got);
+        }
+        uint16_t* y = static_cast<uint16_t*>(a.y) + (t + odd) * a.ldy + r0;
+        if (full && t + 16 <= a.tokens) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                *reinterpret_cast<uint32_t*>(y) = w[i];
+                y += 2 * a.ldy;
+            }
+        } else if (r0 < a.rows) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (t + 2 * i + odd < a.tokens) {
+                    if (r0 + 1 < a.rows) *reinterpret_cast<uint32_t*>(y) = w[i];
+                    else *y = uint16_t(w[i]);
+                }
+                y += 2 * a.ldy;
+            }
+        }
+    } else if (row < a.rows) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (t + i < a.tokens) store_rn(a.y, a.ydtype, (t + i) * a.ldy + row, v[i]);
+    }
+}
+
+// Four rows of one token, the first of them row r, to y.
+__device__ __forceinline__ void gemm_store4(const GemmArgs& a, int64_t t, int64_t r, const float4& v) {
+    const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (r + i < a.rows) store_rn(a.y, a.ydtype, t * a.ldy + r + i, f[i]);
+}
+
+// Adds the cluster's partial sums of one left-over tile, four rows at a time.
+template <int SPLIT>
+__device__ __forceinline__ void gemm_join(const GemmArgs& a, const GemmUnit& w, uint32_t at, int part) {
+    const int64_t t0 = int64_t(w.tt) * a.n;
+    const int live = int(min(int64_t(a.n), a.tokens - t0)) * (kMxTile / 4);
+#pragma unroll 2
+    for (int i = part * kGThreads + threadIdx.x; i < live; i += SPLIT * kGThreads) {
+        float4 p[SPLIT];
+#pragma unroll
+        for (int q = 0; q < SPLIT; ++q) p[q] = ld_cluster_f4(at + i * 16, q);
+        float4 v = p[0];
+#pragma unroll
+        for (int q = 1; q < SPLIT; ++q) {
+            v.x += p[q].x;
+            v.y += p[q].y;
+            v.z += p[q].z;
+            v.w += p[q].w;
+        }
+        gemm_store4(a, t0 + i / (kMxTile / 4), int64_t(w.rt) * kMxTile + i % (kMxTile / 4) * 4, v);
+    }
+}
+
+template <bool PAIR>
+__global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_constant__ CUtensorMap wmap,
+                                                              const __grid_constant__ CUtensorMap xmap,
+                                                              const __grid_constant__ GemmArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align1024(smem_raw);
-    __shared__ uint64_t full[kGMaxStages], empty[kGMaxStages], accum;
+    // full: a stage's bytes are here (two producers); peer: they are in the pair's other CTA too;
+    // empty: its MMAs are done; acc_full: a unit's accumulators are final; acc_free: the columns that
+    // the next unit's buffer shares with them have been read
+    __shared__ uint64_t full[kGMaxStages], peer[PAIR ? kGMaxStages : 1], empty[kGMaxStages], acc_full[2], acc_free;
     __shared__ uint32_t tmem_base;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tile = blockIdx.x / a.split, part = blockIdx.x % a.split;
-    const int rt = tile / a.ntt, tt = tile % a.ntt;
-    const int t0 = tt * a.n;
-    const int k0 = int(int64_t(a.nt) * part / a.split), k1 = int(int64_t(a.nt) * (part + 1) / a.split);
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = PAIR ? int(blockIdx.x & 1) : 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 2);
             mbar_init(&empty[s], 1);
+            if (PAIR) mbar_init(&peer[s], 1);
         }
-        mbar_init(&accum, 1);
+        mbar_init(&acc_full[0], 1);
+        mbar_init(&acc_full[1], 1);
+        mbar_init(&acc_free, PAIR ? 8 : 4);
         fence_mbar_init();
-        prefetch_tensormap(&wmap);
-        prefetch_tensormap(&xmap);
     }
-    if (warp == 1) {
-        tmem_alloc(&tmem_base, a.cols);
-        tmem_relinquish();
+    if (warp == 3) {
+        if (lane == 0) {
+            prefetch_tensormap(&wmap);
+            prefetch_tensormap(&xmap);
+        }
+        __syncwarp();
+        if (PAIR) {
+            tmem_alloc_pair(&tmem_base, a.cols);
+        } else {
+            tmem_alloc(&tmem_base, a.cols);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();      // the other CTA's barriers are ready too
     tc_fence_after();
     const uint32_t tmem = tmem_base;
-    const int xbytes = a.n * kMxTile;
+    const int xrows = PAIR ? a.n / 2 : a.n;      // tokens whose bytes this CTA holds
+    const int xbytes = xrows * kMxTile;
     bool ok = true;
-    if (warp == 0) {
-        if (lane == 0) {
+    GemmUnit w;
+    if (warp == 0 || warp == 2) {
+        int s = 0, issued = 0;
+        uint32_t phase = 1;      // of the empty barriers: the first turn of the ring passes
+        uint8_t* st = smem;
+        const int atoms_all = int((a.tokens + kMxTile - 1) / kMxTile);
+        for (int u = 0; ok && gemm_unit<PAIR>(a, u, w); ++u) {
+            const int t0 = w.tt * a.n;
             const int atom0 = t0 / kMxTile;
-            const int atoms_all = int((a.tokens + kMxTile - 1) / kMxTile);
             const int atoms = min(a.xatoms, atoms_all - atom0);
-            // (the spread weights count with their packed bytes)
-            const uint32_t tx = uint32_t(kMx4TileBytes + xbytes + kMxAtomBytes * (1 + atoms));
-            int k = k0;
-            for (; k < k1; ++k) {
-                const int s = (k - k0) % a.stages, round = (k - k0) / a.stages;
-                if (round > 0) ok = mbar_wait(&empty[s], (round - 1) & 1);
+            const int rt = PAIR ? 2 * w.rt + rank : w.rt;
+            // (a pair's second row tile may not exist: its lines read as zero, its scales are the last tile's)
+            const uint8_t* wsc = a.wsc + int64_t(min(rt, a.rtiles - 1)) * a.nt * kMxAtomBytes;
+            const uint8_t* xsc = a.xsc + int64_t(atom0) * a.nt * kMxAtomBytes;
+            const int line = rt * a.nt * kMxTile;
+            for (int k = w.k0; k < w.k1; k += kGK) {
+                ok = mbar_wait_warp(&empty[s], phase);
                 if (!ok) break;
-                uint8_t* st = smem + int64_t(s) * a.stage_bytes;
-                mbar_arrive_expect_tx(&full[s], tx);
-                tma_load_2d(st, &wmap, &full[s], 0, (rt * a.nt + k) * kMxTile);
-                tma_load_2d(st + kGABytes, &xmap, &full[s], k * kMxTile, t0);
-                uint8_t* sc = st + kGABytes + xbytes;
-                bulk_load(sc, a.wsc + (int64_t(rt) * a.nt + k) * kMxAtomBytes, kMxAtomBytes, &full[s]);
-                for (int i = 0; i < atoms; ++i)
-                    bulk_load(sc + (1 + i) * kMxAtomBytes, a.xsc + (int64_t(atom0 + i) * a.nt + k) * kMxAtomBytes,
-                              kMxAtomBytes, &full[s]);
-            }
-            if (!ok)      // copies in flight land before the CTA ends (bounded)
-                for (int j = max(k0, k - a.stages); j < k; ++j)
-                    mbar_wait(&full[(j - k0) % a.stages], ((j - k0) / a.stages) & 1);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = umma_idesc_mx(kMxTile, a.n);
-            const uint32_t sf_first = tmem + a.cols - a.stages * kGSfCols;
-            const uint32_t xoff = 4 + (t0 % kMxTile) / 32;      // first scale column of the tile's first token
-            for (int k = k0; k < k1 && ok; ++k) {
-                const int s = (k - k0) % a.stages, round = (k - k0) / a.stages;
-                ok = mbar_wait(&full[s], round & 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t st = smem_u32(smem + int64_t(s) * a.stage_bytes);
-                const uint32_t sc = st + kGABytes + xbytes;
-                const uint32_t sf = sf_first + s * kGSfCols;
-                for (int i = 0; i <= a.xatoms; ++i)
-                    tmem_copy_scales(sf + 4 * i, scale_atom_desc(sc + i * kMxAtomBytes));
-                const uint64_t ad = umma_desc_sw128(st), bd = umma_desc_sw128(st + kGABytes);
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    umma_mx(tmem, ad + 2 * b, bd + 2 * b, umma_idesc_scale_id(idesc, b), sf, sf + xoff,
-                            (k > k0 || b > 0) ? 1u : 0u);
-                umma_commit(&empty[s]);
-            }
-            umma_commit(&accum);
-        }
-        __syncwarp();
-    }
-    // (the accumulators are final, and every copy has landed and been read)
-    bool done = true;
-    if (warp >= 1) done = mbar_wait(&accum, 0);
-    tc_fence_after();
-    if (!(ok && done)) set_status(a.status, GALE_ERR_TIMEOUT);
-    const int quarter = warp & 3;
-    const int64_t row = int64_t(rt) * kMxTile + quarter * 32 + lane;
-    const uint32_t lanes = uint32_t(quarter) << 21;
-    if (a.split == 1) {
-        if (warp >= 2) {
-            for (int c = 0; c < a.n; c += 16) {
-                float v[16];
-                tmem_ld16(tmem + lanes + c, v);
-                if (row < a.rows) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (t0 + c + i < a.tokens) store_rn(a.y, a.ydtype, (t0 + c + i) * a.ldy + row, v[i]);
+                const int kt = min(kGK, w.k1 - k);
+                uint8_t* sc = st + kGK * (kGABytes + xbytes);
+                if (warp == 0) {
+                    if (elect_one()) {
+                        // the spread weights count with their packed bytes
+                        mbar_arrive_expect_tx(&full[s], kt * (kMx4TileBytes + kMxAtomBytes));
+                        tma_load_2d(st, &wmap, &full[s], 0, line + k * kMxTile);
+                        if (kt == 2) tma_load_2d(st + kGABytes, &wmap, &full[s], 0, line + (k + 1) * kMxTile);
+                        bulk_load(sc, wsc + k * kMxAtomBytes, kt * kMxAtomBytes, &full[s]);
+                    }
+                } else {
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&full[s], kt * (xbytes + atoms * kMxAtomBytes));
+                        tma_load_2d(st + kGK * kGABytes, &xmap, &full[s], k * kMxTile, t0 + rank * xrows);
+                        if (kt == 2)
+                            tma_load_2d(st + kGK * kGABytes + xbytes, &xmap, &full[s], (k + 1) * kMxTile, t0 + rank * xrows);
+                        for (int j = 0; j < atoms; ++j)
+                            bulk_load(sc + (1 + j) * kGK * kMxAtomBytes, xsc + (int64_t(j) * a.nt + k) * kMxAtomBytes,
+                                      kt * kMxAtomBytes, &full[s]);
+                    }
+                }
+                __syncwarp();
+                ++issued;
+                st += a.stage_bytes;
+                if (++s == a.stages) {
+                    s = 0;
+                    st = smem;
+                    phase ^= 1;
                 }
             }
         }
-    } else {
-        // partial sums [token][128 rows] over the ring, which is no longer in use
-        __syncthreads();
-        float* ps = reinterpret_cast<float*>(smem);
-        if (warp >= 2) {
-            for (int c = 0; c < a.n; c += 16) {
-                float v[16];
-                tmem_ld16(tmem + lanes + c, v);
+        // the last copies land before the CTA may end (bounded)
+        if (!ok)
+            for (int i = max(0, issued - a.stages); i < issued; ++i)
+                mbar_wait_warp(&full[i % a.stages], (i / a.stages) & 1);
+    } else if (warp == 1 && (!PAIR || rank == 0)) {
+        const uint32_t idesc = umma_idesc_mx(PAIR ? 2 * kMxTile : kMxTile, a.n);
+        const uint32_t sf_first = tmem + a.cols - a.stages * a.sfcols;
+        int s = 0;
+        uint32_t phase = 0, st = smem_u32(smem), sf = sf_first;
+        for (int u = 0; ok && gemm_unit<PAIR>(a, u, w); ++u) {
+            const uint32_t d = tmem + ((u & 1) ? a.d1 : 0);
+            const uint32_t xoff = 4 + ((w.tt * a.n) % kMxTile) / 32;      // scale column of the tile's first token
+            if (u > 0) {
+                ok = mbar_wait_warp<PAIR>(&acc_free, (u - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            for (int k = w.k0; k < w.k1; k += kGK) {
+                ok = mbar_wait_warp(&full[s], phase) && (!PAIR || mbar_wait_warp<true>(&peer[s], phase));
+                if (!ok) break;
+                tc_fence_after();
+                const int kt = min(kGK, w.k1 - k);
+                if (elect_one()) {
+                    const uint32_t sc = st + kGK * (kGABytes + xbytes);
+                    for (int j = 0; j < kt; ++j) {
+                        const uint32_t sfj = sf + j * 4 * (1 + a.xatoms);
+                        for (int i = 0; i <= a.xatoms; ++i) {
+                            const uint64_t from = scale_atom_desc(sc + (i * kGK + j) * kMxAtomBytes);
+                            if (PAIR) tmem_copy_scales_pair(sfj + 4 * i, from);
+                            else tmem_copy_scales(sfj + 4 * i, from);
+                        }
+                    }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) ps[(c + i) * kMxTile + quarter * 32 + lane] = v[i];
+                    for (int j = 0; j < kGK; ++j) {
+                        if (j == kt) break;
+                        const uint32_t sfj = sf + j * 4 * (1 + a.xatoms);
+                        const uint64_t ad = umma_desc_sw128(st + j * kGABytes);
+                        const uint64_t bd = umma_desc_sw128(st + kGK * kGABytes + j * xbytes);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const uint32_t more = (k > w.k0 || j > 0 || b > 0) ? 1u : 0u;
+                            const uint32_t id = umma_idesc_scale_id(idesc, b);
+                            if (PAIR) umma_mx_pair(d, ad + 2 * b, bd + 2 * b, id, sfj, sfj + xoff, more);
+                            else umma_mx(d, ad + 2 * b, bd + 2 * b, id, sfj, sfj + xoff, more);
+                        }
+                    }
+                    if (PAIR) umma_commit_pair(&empty[s]);
+                    else umma_commit(&empty[s]);
+                }
+                __syncwarp();
+                st += a.stage_bytes;
+                sf += a.sfcols;
+                if (++s == a.stages) {
+                    s = 0;
+                    st = smem_u32(smem);
+                    sf = sf_first;
+                    phase ^= 1;
+                }
+            }
+            if (elect_one()) {
+                if (PAIR) umma_commit_pair(&acc_full[u & 1]);
+                else umma_commit(&acc_full[u & 1]);
+            }
+            __syncwarp();
+        }
+    } else if (PAIR && warp == 1) {
+        // second CTA of the pair: passes on that its stages have landed
+        int s = 0;
+        uint32_t phase = 0;
+        for (int u = 0; ok && gemm_unit<PAIR>(a, u, w); ++u) {
+            for (int k = w.k0; k < w.k1; k += kGK) {
+                ok = mbar_wait_warp(&full[s], phase);
+                if (!ok) break;
+                if (elect_one()) mbar_arrive_cluster_relaxed(&peer[s], 0);
+                __syncwarp();
+                if (++s == a.stages) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
         }
-        cluster_sync();
-        const int live = int(min(int64_t(a.n), a.tokens - t0)) * kMxTile;
-        const uint32_t base = smem_u32(ps);
-        for (int i = part * kGThreads + threadIdx.x; i < live; i += a.split * kGThreads) {
-            float v = 0.f;
-            for (int q = 0; q < a.split; ++q) v += ld_cluster_f32(base + i * 4, q);
-            const int64_t r = int64_t(rt) * kMxTile + (i & (kMxTile - 1));
-            if (r < a.rows) store_rn(a.y, a.ydtype, int64_t(t0 + i / kMxTile) * a.ldy + r, v);
+    } else if (warp >= 4) {
+        const int quarter = warp & 3;
+        const uint32_t lanes = uint32_t(quarter) << 21;
+        for (int u = 0; ok && gemm_unit<PAIR>(a, u, w); ++u) {
+            ok = mbar_wait_warp(&acc_full[u & 1], (u >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = tmem + lanes + ((u & 1) ? a.d1 : 0);
+            const int64_t row = int64_t(PAIR ? 2 * w.rt + rank : w.rt) * kMxTile + quarter * 32 + lane;
+            const bool rows_full = row - lane + 32 <= a.rows;
+            float* ps = nullptr;
+            if (w.joint)     // partial sums [token][128 rows] over the ring (the last unit) or behind it
+                ps = reinterpret_cast<float*>(smem + (a.joint > 1 ? int64_t(a.stages) * a.stage_bytes : 0)) +
+                     int64_t(u - a.whole) * a.n * kMxTile + quarter * 32 + lane;
+            const int64_t t0 = int64_t(w.tt) * a.n;
+            auto put = [&](int c, const float (&v)[16]) {
+                if (ps) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) ps[(c + i) * kMxTile] = v[i];
+                } else if (t0 + c < a.tokens) {
+                    gemm_store16(a, t0 + c, row, lane, rows_full, v);
+                }
+            };
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_cluster(&acc_free, 0);
+                    else mbar_arrive(&acc_free);
+                }
+            };
+            // the columns that the other buffer shares (the last n - d1 of buffer 0, the first of buffer 1) go
+            // to registers first, so that the next unit's MMAs wait for no store
+            const int shared = a.n - a.d1;
+            const int c0 = (u & 1) ? 0 : a.d1;
+            if (shared > 0) {
+                float v[kGMaxShared / 16][16];
+#pragma unroll
+                for (int q = 0; q < kGMaxShared / 16; ++q)
+                    if (16 * q < shared) tmem_ld16_start(d + c0 + 16 * q, v[q]);
+                tmem_wait_ld();
+                release();
+#pragma unroll
+                for (int q = 0; q < kGMaxShared / 16; ++q)
+                    if (16 * q < shared) put(c0 + 16 * q, v[q]);
+            } else {
+                release();
+            }
+            const int c1 = (u & 1) ? max(shared, 0) : 0, c2 = (u & 1) ? a.n : min(a.n, a.d1);
+            for (int c = c1; c < c2; c += 16) {
+                float v[16];
+                tmem_ld16(d + c, v);
+                put(c, v);
+            }
         }
-        cluster_sync();      // the peers have read this CTA's partial sums
+    }
+    if (!ok) set_status(a.status, GALE_ERR_TIMEOUT);
+    if (!PAIR && a.split > 1) {
+        cluster_sync();
+        const int part = blockIdx.x % a.split;
+        uint32_t at = smem_u32(smem) + (a.joint > 1 ? a.stages * a.stage_bytes : 0);
+        for (int u = a.whole; gemm_unit<PAIR>(a, u, w); ++u, at += a.n * kMxTile * 4) {
+            if (a.split == 2) gemm_join<2>(a, w, at, part);
+            else if (a.split == 4) gemm_join<4>(a, w, at, part);
+            else gemm_join<8>(a, w, at, part);
+        }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_dealloc(tmem, a.cols);
-}
-
-// Tokens of a tile: all of them up to 256 (the MMA's N in steps of 16), equal
-// tiles of a multiple of 64 beyond (a tile's first scale sits at an even TMEM column).
-int gemm_tile_tokens(int64_t tokens) {
-    if (tokens <= kGMaxN) return int(align_up(tokens, 16));
-    const int64_t tiles = (tokens + kGMaxN - 1) / kGMaxN;
-    return int(align_up((tokens + tiles - 1) / tiles, 64));
+    // nobody reads a peer's partial sums, reads its operands or arrives on its barriers after this
+    if (PAIR || a.split > 1) cluster_sync();
+    if (warp == 3) {
+        tc_fence_after();
+        if (PAIR) tmem_dealloc_pair(tmem, a.cols);
+        else tmem_dealloc(tmem, a.cols);
+    }
 }
 
 struct GemmPlan {
     GemmArgs a;
-    int64_t grid;
-    int smem;
+    bool pair;
+    int grid, smem;
 };
 
-void gemm_plan(int64_t rows, int nt, int64_t tokens, GemmPlan& p) {
+// Tokens of a tile: all of them up to `most` (the MMA's N in steps of 16), equal
+// tiles of a multiple of 64 beyond (a tile's first scale sits at an even TMEM column).
+int gemm_tile_tokens(int64_t tokens, int most) {
+    if (tokens <= most) return int(align_up(tokens, 16));
+    const int64_t tiles = (tokens + most - 1) / most;
+    return int(align_up((tokens + tiles - 1) / tiles, 64));
+}
+
+// Clusters of `size` CTAs of this kernel that the device holds at once (an SM
+// that is left over in its group of SMs holds none of a larger cluster).
+int gemm_clusters(int size) {
+    static int found[64][4] = {};       // per device, by log2 of the size: an attribute of the device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    const int slot = size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : 3;
+    if (!found[dev][slot]) {
+        int n = 0;
+        if (ensure_smem(reinterpret_cast<const void*>(mx_gemm_kernel<false>), kGSmemSm) != GALE_OK) return 0;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(unsigned(size) * 16);
+        cfg.blockDim = dim3(kGThreads);
+        cfg.dynamicSmemBytes = kGSmemSm;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim = {unsigned(size), 1, 1};
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, mx_gemm_kernel<false>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        found[dev][slot] = n;
+    }
+    return found[dev][slot];
+}
+
+// False if the device does not answer.
+bool gemm_plan(int64_t rows, int nt, int64_t tokens, GemmPlan& p) {
     GemmArgs& a = p.a;
     a.rows = rows;
     a.tokens = tokens;
     a.nt = nt;
-    a.n = gemm_tile_tokens(tokens);
+    a.rtiles = int((rows + kMxTile - 1) / kMxTile);
+    p.pair = tokens > kGMaxN;
+    a.n = gemm_tile_tokens(tokens, kGMaxN);
     a.ntt = int((tokens + a.n - 1) / a.n);
     // tokens t0 .. t0 + n - 1 of a tile that starts at a multiple of n
     a.xatoms = a.ntt == 1 ? (a.n + kMxTile - 1) / kMxTile : a.n % kMxTile == 0 ? a.n / kMxTile : a.n / kMxTile + 2;
     if (a.xatoms > 3) a.xatoms = 3;
-    const int64_t tiles = (rows + kMxTile - 1) / kMxTile * a.ntt;
+    a.tiles = (p.pair ? (a.rtiles + 1) / 2 : a.rtiles) * a.ntt;
+    int join_bytes = 0;
     a.split = 1;
-    if (a.n <= 64)
-        while (a.split < 8 && tiles * a.split < 2 * sm_count() && nt / (a.split * 2) >= 4) a.split *= 2;
-    a.stage_bytes = int(align_up(kGABytes + a.n * kMxTile + kMxAtomBytes * (1 + a.xatoms), 1024));
-    // small tiles: two CTAs per SM, so that one's start and end overlap the other's stream
-    const int room = (a.n <= 64 ? kGSmemSm / 2 : kGSmemSm) - 2048;
-    a.stages = room / a.stage_bytes;
+    if (p.pair) {
+        a.workers = gemm_clusters(2);
+        if (a.workers < 1) return false;
+        if (a.workers > a.tiles) a.workers = a.tiles;
+        a.whole = (a.tiles + a.workers - 1) / a.workers;
+        a.joint = 0;
+        p.grid = 2 * a.workers;
+    } else {
+        // The cluster that makes the longest CTA shortest, in column tiles; a join costs about as much as
+        // six of them, and one more for every 32 tokens.
+        int64_t best = INT64_MAX;
+        for (int s = 1; s <= 8; s *= 2) {
+            const int clusters = gemm_clusters(s), workers = clusters * s;
+            if (clusters < 1) return false;
+            const int whole = s == 1 ? (a.tiles + workers - 1) / workers : a.tiles / workers;
+            const int left = s == 1 ? 0 : a.tiles - whole * workers;
+            const int joint = (left + clusters - 1) / clusters;
+            if (s > 1 && (joint == 0 || nt < 2 * kGK * s)) continue;
+            const int64_t bytes = joint > 1 ? int64_t(joint) * a.n * kMxTile * 4 : 0;
+            if (bytes > 64 * 1024) continue;
+            const int64_t cost = int64_t(whole) * nt + int64_t(joint) * ((nt + s - 1) / s) + (joint ? 6 + a.n / 32 : 0);
+            if (cost < best) {
+                best = cost;
+                a.split = s;
+                a.workers = workers;
+                a.whole = whole;
+                a.joint = joint;
+                join_bytes = int(bytes);
+            }
+        }
+        if (a.split == 1 && a.workers > a.tiles) a.workers = a.tiles;
+        // clusters without a tile are not launched
+        if (a.split > 1 && a.whole == 0 && a.tiles < a.workers / a.split) a.workers = a.tiles * a.split;
+        p.grid = a.workers;
+    }
+    const int xrows = p.pair ? a.n / 2 : a.n;
+    a.stage_bytes = int(align_up(kGK * (kGABytes + xrows * kMxTile + kMxAtomBytes * (1 + a.xatoms)), 1024));
+    a.stages = (kGSmemSm - 1024 - join_bytes) / a.stage_bytes;
     if (a.stages > kGMaxStages) a.stages = kGMaxStages;
+    a.sfcols = kGK * 4 * (1 + a.xatoms);
+    const int units = a.whole + a.joint;
     int cols = 32;
-    while (cols < a.n + a.stages * kGSfCols) cols *= 2;
+    while (cols < (units > 1 ? 2 : 1) * a.n + a.stages * a.sfcols && cols < 512) cols *= 2;
     a.cols = cols;
-    p.smem = a.stages * a.stage_bytes + 1024;
+    const int avail = (cols - a.stages * a.sfcols) / 16 * 16;
+    a.d1 = units == 1 || avail >= 2 * a.n ? a.n : avail - a.n;
+    p.smem = a.stages * a.stage_bytes + join_bytes + 1024;
     // As large a share of the SM's shared memory as of its TMEM, so that a CTA
     // that is resident never waits for TMEM columns.
     const int least = int(int64_t(kGSmemSm) * cols / 512);
     if (p.smem < least) p.smem = least;
-    p.grid = tiles * a.split;
+    return a.n - a.d1 <= kGMaxShared;
 }
 
 }  // namespace
@@ -241,9 +561,9 @@ extern "C" int gale_mx_gemm(const void* w4, int64_t rows, int64_t cols, const vo
     if (!aligned(ws, 256)) return GALE_ERR_ALIGN;
     const uint8_t* w = static_cast<const uint8_t*>(w4);
     const uint8_t* x = static_cast<const uint8_t*>(x8);
+    if (rows * tokens > (int64_t(1) << 44)) return GALE_ERR_UNSUPPORTED;   // (tiles are counted in 32 bits)
     GemmPlan p{};
-    gemm_plan(rows, int(W.cols_padded / kMxTile), tokens, p);
-    if (p.grid > INT32_MAX) return GALE_ERR_UNSUPPORTED;
+    if (!gemm_plan(rows, int(W.cols_padded / kMxTile), tokens, p)) return GALE_ERR_CUDA;
     p.a.wsc = w + W.s_offset;
     p.a.xsc = x + X.s_offset;
     p.a.y = y;
@@ -252,9 +572,11 @@ extern "C" int gale_mx_gemm(const void* w4, int64_t rows, int64_t cols, const vo
     p.a.ydtype = y_dtype;
     CUtensorMap wmap, xmap;
     int rc = make_map_mx4(&wmap, w, W.q_bytes / (kMxTile / 2));
-    if (rc == GALE_OK) rc = make_map_bytes(&xmap, x, W.cols_padded, tokens, kMxTile, p.a.n);
+    if (rc == GALE_OK) rc = make_map_bytes(&xmap, x, W.cols_padded, tokens, kMxTile, p.pair ? p.a.n / 2 : p.a.n);
     if (rc != GALE_OK) return rc;
-    if (ensure_smem(reinterpret_cast<const void*>(mx_gemm_kernel), p.smem) != GALE_OK) return GALE_ERR_CUDA;
+    p.a.pair16 = ldy % 2 == 0 && aligned(y, 4);
+    auto kern = p.pair ? mx_gemm_kernel<true> : mx_gemm_kernel<false>;
+    if (ensure_smem(reinterpret_cast<const void*>(kern), p.smem) != GALE_OK) return GALE_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(p.grid));
     cfg.blockDim = dim3(kGThreads);
@@ -262,10 +584,10 @@ extern "C" int gale_mx_gemm(const void* w4, int64_t rows, int64_t cols, const vo
     cfg.stream = as_stream(stream);
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {unsigned(p.a.split), 1, 1};
+    at[0].val.clusterDim = {unsigned(p.pair ? 2 : p.a.split), 1, 1};
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, mx_gemm_kernel, wmap, xmap, p.a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kern, wmap, xmap, p.a) != cudaSuccess) {
         cudaGetLastError();      // reported here, not by the next call
         return GALE_ERR_CUDA;
     }

@@ -506,7 +506,7 @@ int gale_w4_gemv(const void* packed, int64_t rows, int64_t cols, const uint16_t*
  * bytes (columns past cols zero), s as above with rows = tokens (the scales of
  * rows past the last token are never written nor used).
  * Sections and totals are 256-byte aligned.  1 <= rows <= 2^24,
- * 1 <= cols <= 2^20, and (padded rows / 128) * padded cols < 2^31.
+ * 1 <= cols <= 2^20, and (padded rows / 128) * padded cols < 2^30.
  * ------------------------------------------------------------------------- */
 typedef struct {
     int64_t rows, cols, cols_padded;
@@ -546,9 +546,11 @@ int gale_mx8_quantize(const void* x, int x_dtype, int64_t ld, int64_t tokens, in
  *        first int32 is a sticky status word: the caller sets it to 0 once, the
  *        call never clears it and writes GALE_ERR_TIMEOUT there if a bounded
  *        wait inside the kernel ran out (results are then undefined)
- * Any token count (0 is a no-op).  The sums' order depends on the sizes alone:
+ * Any token count (0 is a no-op; GALE_ERR_UNSUPPORTED where rows * tokens
+ * passes 2^44).  The sums' order depends on the sizes alone:
  * equal calls give equal bits.
- * Errors: GALE_ERR_ARG, GALE_ERR_ALIGN, GALE_ERR_WORKSPACE, GALE_ERR_CUDA. */
+ * Errors: GALE_ERR_ARG, GALE_ERR_ALIGN, GALE_ERR_WORKSPACE,
+ * GALE_ERR_UNSUPPORTED, GALE_ERR_CUDA. */
 size_t gale_mx_gemm_workspace_size(int64_t rows, int64_t cols, int64_t tokens);   /* host only; 0 on invalid sizes */
 int gale_mx_gemm(const void* w4, int64_t rows, int64_t cols, const void* x8, int64_t tokens, void* y,
                  int y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream);

@@ -143,7 +143,10 @@ def _check(y, want, mag, cols, out):
     (256, 4096, 1, "f32"), (256, 4096, 8, "bf16"), (2048, 4096, 8, "f32"), (300, 1000, 17, "f16"),
     (257, 640, 33, "f32"), (512, 512, 64, "bf16"), (384, 2048, 100, "f32"), (128, 256, 128, "f32"),
     (200, 260, 129, "bf16"), (640, 384, 255, "f32"), (1000, 777, 300, "f16"), (129, 4096, 257, "f32"),
-    (4100, 512, 700, "f32"), (64, 16384, 5, "f32"), (2050, 4000, 513, "bf16")])
+    (4100, 512, 700, "f32"), (64, 16384, 5, "f32"), (2050, 4000, 513, "bf16"),
+    # several tiles per CTA, alone and with left-over tiles that clusters share
+    (38000, 300, 3, "f32"), (12800, 1024, 16, "bf16"), (20000, 260, 60, "f32"), (19072, 512, 200, "f32"),
+    (5000, 200, 2100, "f32"), (3000, 390, 4000, "bf16"), (130, 130, 10000, "f16")])
 def test_gemm_parity(rows, cols, tokens, out):
     w, x = _matrix(rows, cols, rows * 7 + cols, scale=0.02), _matrix(tokens, cols, tokens, "bf16", 3.0)
     y = _gemm(_pack4(w), rows, cols, _pack8(x), tokens, out)
