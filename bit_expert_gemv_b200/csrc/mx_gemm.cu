@@ -9,8 +9,8 @@
 // weights' stream from HBM, many by the tensor pipe.
 //
 // The kernel is persistent, one CTA per SM.  Roles (256 threads): warps 0 and 2
-// fill a ring of stages (256 columns each) with weights and with tokens; a lane
-// of warp 1 copies a stage's scales to TMEM and issues its eight MMAs; warps
+// fill a ring of stages (256 columns each) with weights and with tokens;
+// warp 1 copies a stage's scales to TMEM and issues its eight MMAs; warps
 // 4-7 read a tile's accumulators and write y while the next tile's MMAs run
 // into the other accumulator buffer.  What a few instructions of one lane cost
 // sets the pace of the rings: a turn of a producer's loop takes some 400 cycles
@@ -221,10 +221,13 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
     const int xbytes = xrows * kMxTile;
     bool ok = true;
     GemmUnit w;
+    const uint32_t ring = smem_u32(smem), ring_end = ring + a.stages * a.stage_bytes;
+    const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), peer0 = smem_u32(peer);
     if (warp == 0 || warp == 2) {
-        int s = 0, issued = 0;
-        uint32_t phase = 1;      // of the empty barriers: the first turn of the ring passes
-        uint8_t* st = smem;
+        const bool lead = elect_one();
+        int issued = 0;
+        // (st, s8: the stage's shared memory and the offset of its barriers)
+        uint32_t st = ring, s8 = 0, phase = 1;      // of the empty barriers: the first turn of the ring passes
         const int atoms_all = int((a.tokens + kMxTile - 1) / kMxTile);
         for (int u = 0; ok && gemm_unit<PAIR>(a, u, w); ++u) {
             const int t0 = w.tt * a.n;
@@ -236,35 +239,32 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
             const uint8_t* xsc = a.xsc + int64_t(atom0) * a.nt * kMxAtomBytes;
             const int line = rt * a.nt * kMxTile;
             for (int k = w.k0; k < w.k1; k += kGK) {
-                ok = mbar_wait_warp(&empty[s], phase);
+                ok = mbar_wait_warp(empty0 + s8, phase);
                 if (!ok) break;
                 const int kt = min(kGK, w.k1 - k);
-                uint8_t* sc = st + kGK * (kGABytes + xbytes);
+                const uint32_t bar = full0 + s8;
+                const uint32_t sc = st + kGK * (kGABytes + xbytes);
                 if (warp == 0) {
-                    if (elect_one()) {
-                        // the spread weights count with their packed bytes
-                        mbar_arrive_expect_tx(&full[s], kt * (kMx4TileBytes + kMxAtomBytes));
-                        tma_load_2d(st, &wmap, &full[s], 0, line + k * kMxTile);
-                        if (kt == 2) tma_load_2d(st + kGABytes, &wmap, &full[s], 0, line + (k + 1) * kMxTile);
-                        bulk_load(sc, wsc + k * kMxAtomBytes, kt * kMxAtomBytes, &full[s]);
-                    }
+                    // the spread weights count with their packed bytes
+                    mbar_expect_lead(lead, bar, kt * (kMx4TileBytes + kMxAtomBytes));
+                    tma_load_2d(lead, st, &wmap, bar, 0, line + k * kMxTile);
+                    if (kt == 2) tma_load_2d(lead, st + kGABytes, &wmap, bar, 0, line + (k + 1) * kMxTile);
+                    bulk_load_lead(lead, sc, wsc + k * kMxAtomBytes, kt * kMxAtomBytes, bar);
                 } else {
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&full[s], kt * (xbytes + atoms * kMxAtomBytes));
-                        tma_load_2d(st + kGK * kGABytes, &xmap, &full[s], k * kMxTile, t0 + rank * xrows);
-                        if (kt == 2)
-                            tma_load_2d(st + kGK * kGABytes + xbytes, &xmap, &full[s], (k + 1) * kMxTile, t0 + rank * xrows);
-                        for (int j = 0; j < atoms; ++j)
-                            bulk_load(sc + (1 + j) * kGK * kMxAtomBytes, xsc + (int64_t(j) * a.nt + k) * kMxAtomBytes,
-                                      kt * kMxAtomBytes, &full[s]);
-                    }
+                    const uint32_t xs = st + kGK * kGABytes;
+                    mbar_expect_lead(lead, bar, kt * (xbytes + atoms * kMxAtomBytes));
+                    tma_load_2d(lead, xs, &xmap, bar, k * kMxTile, t0 + rank * xrows);
+                    if (kt == 2) tma_load_2d(lead, xs + xbytes, &xmap, bar, (k + 1) * kMxTile, t0 + rank * xrows);
+                    for (int j = 0; j < atoms; ++j)
+                        bulk_load_lead(lead, sc + (1 + j) * kGK * kMxAtomBytes,
+                                       xsc + (int64_t(j) * a.nt + k) * kMxAtomBytes, kt * kMxAtomBytes, bar);
                 }
-                __syncwarp();
                 ++issued;
                 st += a.stage_bytes;
-                if (++s == a.stages) {
-                    s = 0;
-                    st = smem;
+                s8 += 8;
+                if (st == ring_end) {
+                    st = ring;
+                    s8 = 0;
                     phase ^= 1;
                 }
             }
@@ -272,80 +272,77 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
         // the last copies land before the CTA may end (bounded)
         if (!ok)
             for (int i = max(0, issued - a.stages); i < issued; ++i)
-                mbar_wait_warp(&full[i % a.stages], (i / a.stages) & 1);
+                mbar_wait_warp(full0 + i % a.stages * 8, (i / a.stages) & 1);
     } else if (warp == 1 && (!PAIR || rank == 0)) {
+        const bool lead = elect_one();
         const uint32_t idesc = umma_idesc_mx(PAIR ? 2 * kMxTile : kMxTile, a.n);
         const uint32_t sf_first = tmem + a.cols - a.stages * a.sfcols;
-        int s = 0;
-        uint32_t phase = 0, st = smem_u32(smem), sf = sf_first;
+        const uint64_t xstep = xbytes >> 4;
+        uint32_t st = ring, s8 = 0, phase = 0, sf = sf_first;
         for (int u = 0; ok && gemm_unit<PAIR>(a, u, w); ++u) {
             const uint32_t d = tmem + ((u & 1) ? a.d1 : 0);
             const uint32_t xoff = 4 + ((w.tt * a.n) % kMxTile) / 32;      // scale column of the tile's first token
             if (u > 0) {
-                ok = mbar_wait_warp<PAIR>(&acc_free, (u - 1) & 1);
+                ok = mbar_wait_warp<PAIR>(smem_u32(&acc_free), (u - 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
             }
             for (int k = w.k0; k < w.k1; k += kGK) {
-                ok = mbar_wait_warp(&full[s], phase) && (!PAIR || mbar_wait_warp<true>(&peer[s], phase));
+                ok = mbar_wait_warp(full0 + s8, phase) && (!PAIR || mbar_wait_warp<true>(peer0 + s8, phase));
                 if (!ok) break;
                 tc_fence_after();
                 const int kt = min(kGK, w.k1 - k);
-                if (elect_one()) {
-                    const uint32_t sc = st + kGK * (kGABytes + xbytes);
-                    for (int j = 0; j < kt; ++j) {
-                        const uint32_t sfj = sf + j * 4 * (1 + a.xatoms);
-                        for (int i = 0; i <= a.xatoms; ++i) {
-                            const uint64_t from = scale_atom_desc(sc + (i * kGK + j) * kMxAtomBytes);
-                            if (PAIR) tmem_copy_scales_pair(sfj + 4 * i, from);
-                            else tmem_copy_scales(sfj + 4 * i, from);
-                        }
-                    }
+                const uint64_t from = scale_atom_desc(st + kGK * (kGABytes + xbytes));
+                const uint64_t ad = umma_desc_sw128(st), bd = umma_desc_sw128(st + kGK * kGABytes);
 #pragma unroll
-                    for (int j = 0; j < kGK; ++j) {
-                        if (j == kt) break;
-                        const uint32_t sfj = sf + j * 4 * (1 + a.xatoms);
-                        const uint64_t ad = umma_desc_sw128(st + j * kGABytes);
-                        const uint64_t bd = umma_desc_sw128(st + kGK * kGABytes + j * xbytes);
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const uint32_t more = (k > w.k0 || j > 0 || b > 0) ? 1u : 0u;
-                            const uint32_t id = umma_idesc_scale_id(idesc, b);
-                            if (PAIR) umma_mx_pair(d, ad + 2 * b, bd + 2 * b, id, sfj, sfj + xoff, more);
-                            else umma_mx(d, ad + 2 * b, bd + 2 * b, id, sfj, sfj + xoff, more);
-                        }
+                for (int j = 0; j < kGK; ++j) {
+                    if (j == kt) break;
+                    const uint32_t sfj = sf + j * 4 * (1 + a.xatoms);
+                    for (int i = 0; i <= a.xatoms; ++i) {
+                        if (PAIR) tmem_copy_scales_pair(lead, sfj + 4 * i, from + (i * kGK + j) * (kMxAtomBytes >> 4));
+                        else tmem_copy_scales(lead, sfj + 4 * i, from + (i * kGK + j) * (kMxAtomBytes >> 4));
                     }
-                    if (PAIR) umma_commit_pair(&empty[s]);
-                    else umma_commit(&empty[s]);
                 }
-                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < kGK; ++j) {
+                    if (j == kt) break;
+                    const uint32_t sfj = sf + j * 4 * (1 + a.xatoms);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const uint32_t more = (k > w.k0 || j > 0 || b > 0) ? 1u : 0u;
+                        const uint32_t id = umma_idesc_scale_id(idesc, b);
+                        const uint64_t aj = ad + j * (kGABytes >> 4) + 2 * b, bj = bd + j * xstep + 2 * b;
+                        if (PAIR) umma_mx_pair(lead, d, aj, bj, id, sfj, sfj + xoff, more);
+                        else umma_mx(lead, d, aj, bj, id, sfj, sfj + xoff, more);
+                    }
+                }
+                if (PAIR) umma_commit_pair(lead, &empty[0] + (s8 >> 3));
+                else umma_commit_one(lead, &empty[0] + (s8 >> 3));
                 st += a.stage_bytes;
+                s8 += 8;
                 sf += a.sfcols;
-                if (++s == a.stages) {
-                    s = 0;
-                    st = smem_u32(smem);
+                if (st == ring_end) {
+                    st = ring;
+                    s8 = 0;
                     sf = sf_first;
                     phase ^= 1;
                 }
             }
-            if (elect_one()) {
-                if (PAIR) umma_commit_pair(&acc_full[u & 1]);
-                else umma_commit(&acc_full[u & 1]);
-            }
-            __syncwarp();
+            if (PAIR) umma_commit_pair(lead, &acc_full[u & 1]);
+            else umma_commit_one(lead, &acc_full[u & 1]);
         }
     } else if (PAIR && warp == 1) {
         // second CTA of the pair: passes on that its stages have landed
-        int s = 0;
-        uint32_t phase = 0;
+        uint32_t s8 = 0, phase = 0;
         for (int u = 0; ok && gemm_unit<PAIR>(a, u, w); ++u) {
             for (int k = w.k0; k < w.k1; k += kGK) {
-                ok = mbar_wait_warp(&full[s], phase);
+                ok = mbar_wait_warp(full0 + s8, phase);
                 if (!ok) break;
-                if (elect_one()) mbar_arrive_cluster_relaxed(&peer[s], 0);
+                if (lane == 0) mbar_arrive_cluster_relaxed(peer0 + s8, 0);
                 __syncwarp();
-                if (++s == a.stages) {
-                    s = 0;
+                s8 += 8;
+                if (s8 == uint32_t(a.stages) * 8) {
+                    s8 = 0;
                     phase ^= 1;
                 }
             }
@@ -354,7 +351,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
         const int quarter = warp & 3;
         const uint32_t lanes = uint32_t(quarter) << 21;
         for (int u = 0; ok && gemm_unit<PAIR>(a, u, w); ++u) {
-            ok = mbar_wait_warp(&acc_full[u & 1], (u >> 1) & 1);
+            ok = mbar_wait_warp(smem_u32(&acc_full[u & 1]), (u >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + lanes + ((u & 1) ? a.d1 : 0);
@@ -377,7 +374,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (PAIR) mbar_arrive_cluster(&acc_free, 0);
+                    if (PAIR) mbar_arrive_cluster_relaxed(smem_u32(&acc_free), 0);
                     else mbar_arrive(&acc_free);
                 }
             };
