@@ -12,31 +12,34 @@ namespace {
 // One 128 x 128 tile per CTA: 16 threads of 8 columns per row, 16 rows a pass,
 // all eight passes' loads in flight before the first is used.  Bound by HBM:
 // it reads the matrix once and writes 0.53 bytes per element.
-__global__ void __launch_bounds__(256) mx4_quantize_kernel(const void* __restrict__ w, int dtype, int64_t ld,
-                                                           int64_t rows, int64_t cols, int vec,
-                                                           uint8_t* __restrict__ q, uint32_t* __restrict__ s) {
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(256) mx4_quantize_kernel(const void* __restrict__ w, int64_t ld, int64_t rows,
+                                                           int64_t cols, uint8_t* __restrict__ q,
+                                                           uint32_t* __restrict__ s) {
     const int64_t nt = (cols + kMxTile - 1) / kMxTile;
     const int64_t tile = blockIdx.x;
     const int64_t r0 = tile / nt * kMxTile, c0 = tile % nt * kMxTile;
     const int tr = threadIdx.x >> 4, tc = (threadIdx.x & 15) * 8;
     const int64_t left = cols - c0 - tc;
     const int n = left >= 8 ? 8 : left > 0 ? int(left) : 0;
-    float v[8][8];
+    Raw8<DT> raw[8];
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
         const int64_t r = r0 + p * 16 + tr;
-        load8(w, dtype, r * ld + c0 + tc, r < rows ? n : 0, vec, v[p]);
+        load_raw8<DT, VEC>(w, r * ld + c0 + tc, r < rows ? n : 0, raw[p]);
     }
     uint8_t* qt = q + tile * kMx4TileBytes;
     uint32_t* st = s + tile * (kMxAtomBytes / 4);
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
         const int r = p * 16 + tr;
-        uint32_t m = amax8_bits(v[p]);
+        float v[8];
+        raw8_f32<DT>(raw[p], v);
+        uint32_t m = amax8_bits(v);
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const uint32_t b = mx4_scale_byte(m);
-        *reinterpret_cast<uint32_t*>(qt + r * (kMxTile / 2) + tc / 2) = b == 255u ? 0u : mx4_codes(v[p], mx_inverse(b));
+        *reinterpret_cast<uint32_t*>(qt + r * (kMxTile / 2) + tc / 2) = b == 255u ? 0u : mx4_codes(v, mx_inverse(b));
         // the row's four scale bytes, one per four threads, as one word
         uint32_t word = b << (8 * ((threadIdx.x >> 2) & 3));
         word |= __shfl_xor_sync(0xffffffffu, word, 4);
@@ -83,33 +86,35 @@ __global__ void __launch_bounds__(256) mx4_unpack_kernel(const uint8_t* __restri
 // Tokens: 16 threads of 8 columns per (row, 128 columns); the columns up to the
 // next multiple of 128 are written as zeros with scale byte 0.
 constexpr int kQ8Passes = 4;   // 64 rows per CTA
-__global__ void __launch_bounds__(256) mx8_quantize_kernel(const void* __restrict__ x, int dtype, int64_t ld,
-                                                           int64_t tokens, int64_t cols, int vec,
-                                                           uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(256) mx8_quantize_kernel(const void* __restrict__ x, int64_t ld, int64_t tokens,
+                                                           int64_t cols, uint8_t* __restrict__ q,
+                                                           uint8_t* __restrict__ s) {
     const int64_t nt = (cols + kMxTile - 1) / kMxTile;
     const int64_t ct = blockIdx.x % nt;
     const int64_t r0 = blockIdx.x / nt * (16 * kQ8Passes);
     const int tr = threadIdx.x >> 4, tc = (threadIdx.x & 15) * 8;
     const int64_t left = cols - ct * kMxTile - tc;
     const int n = left >= 8 ? 8 : left > 0 ? int(left) : 0;
-    float v[kQ8Passes][8];
+    Raw8<DT> raw[kQ8Passes];
 #pragma unroll
     for (int p = 0; p < kQ8Passes; ++p) {
         const int64_t r = r0 + p * 16 + tr;
-        load8(x, dtype, r * ld + ct * kMxTile + tc, r < tokens ? n : 0, vec, v[p]);
+        load_raw8<DT, VEC>(x, r * ld + ct * kMxTile + tc, r < tokens ? n : 0, raw[p]);
     }
 #pragma unroll
     for (int p = 0; p < kQ8Passes; ++p) {
         const int64_t r = r0 + p * 16 + tr;
-        uint32_t m = amax8_bits(v[p]);
+        float v[8];
+        raw8_f32<DT>(raw[p], v);
+        uint32_t m = amax8_bits(v);
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const uint32_t b = mx8_scale_byte(m);
         const float inv = mx_inverse(b);
         uint2 c = make_uint2(0u, 0u);
         if (b != 255u)
-            c = make_uint2(mx8_codes(v[p][0], v[p][1], v[p][2], v[p][3], inv),
-                           mx8_codes(v[p][4], v[p][5], v[p][6], v[p][7], inv));
+            c = make_uint2(mx8_codes(v[0], v[1], v[2], v[3], inv), mx8_codes(v[4], v[5], v[6], v[7], inv));
         uint32_t word = b << (8 * ((threadIdx.x >> 2) & 3));
         word |= __shfl_xor_sync(0xffffffffu, word, 4);
         word |= __shfl_xor_sync(0xffffffffu, word, 8);
@@ -168,8 +173,10 @@ extern "C" int gale_mx4_quantize(const void* w, int w_dtype, int64_t ld, int64_t
     if (!aligned(packed, 256) || !aligned(w, dtype_size(w_dtype))) return GALE_ERR_ALIGN;
     uint8_t* b = static_cast<uint8_t*>(packed);
     const int64_t tiles = L.q_bytes / kMx4TileBytes;
-    mx4_quantize_kernel<<<unsigned(tiles), 256, 0, as_stream(stream)>>>(
-        w, w_dtype, ld, rows, cols, rows_vec(w, w_dtype, ld), b, reinterpret_cast<uint32_t*>(b + L.s_offset));
+    by_dtype_vec(w_dtype, rows_vec(w, w_dtype, ld), [&](auto dt, auto vec) {
+        mx4_quantize_kernel<decltype(dt)::value, decltype(vec)::value><<<unsigned(tiles), 256, 0, as_stream(stream)>>>(
+            w, ld, rows, cols, b, reinterpret_cast<uint32_t*>(b + L.s_offset));
+    });
     GALE_LAUNCH_CHECK();
     return GALE_OK;
 }
@@ -200,8 +207,10 @@ extern "C" int gale_mx8_quantize(const void* x, int x_dtype, int64_t ld, int64_t
     uint8_t* b = static_cast<uint8_t*>(packed);
     const int64_t rows_cta = 16 * kQ8Passes;
     const int64_t grid = (tokens + rows_cta - 1) / rows_cta * (L.cols_padded / kMxTile);
-    mx8_quantize_kernel<<<unsigned(grid), 256, 0, as_stream(stream)>>>(x, x_dtype, ld, tokens, cols,
-                                                                       rows_vec(x, x_dtype, ld), b, b + L.s_offset);
+    by_dtype_vec(x_dtype, rows_vec(x, x_dtype, ld), [&](auto dt, auto vec) {
+        mx8_quantize_kernel<decltype(dt)::value, decltype(vec)::value><<<unsigned(grid), 256, 0, as_stream(stream)>>>(
+            x, ld, tokens, cols, b, b + L.s_offset);
+    });
     GALE_LAUNCH_CHECK();
     return GALE_OK;
 }

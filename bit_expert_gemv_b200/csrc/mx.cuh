@@ -10,6 +10,8 @@
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace gale {
@@ -66,34 +68,66 @@ __device__ __forceinline__ uint32_t mx8_codes(float a, float b, float c, float d
     return lo | hi << 16;
 }
 
-// Eight consecutive elements from element offset `at`, of which the first `n`
-// exist; the others read as zero.  `vec`: the eight may be read 16 bytes at a time.
-__device__ __forceinline__ void load8(const void* p, int dtype, int64_t at, int n, bool vec, float (&v)[8]) {
-    if (vec && n >= 8) {
-        if (dtype == GALE_F32) {
-            const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-            const float4 a = q[0], b = q[1];
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// Eight consecutive elements of type DT as loaded: several rows' loads can be in
+// flight before the first is converted.
+template <int DT>
+struct Raw8 {
+    uint32_t u[DT == GALE_F32 ? 8 : 4];
+};
+// The elements from offset `at`, of which the first `n` exist; the others are
+// zero.  VEC: they may be read 16 bytes at a time.
+template <int DT, bool VEC>
+__device__ __forceinline__ void load_raw8(const void* p, int64_t at, int n, Raw8<DT>& v) {
+    if (VEC && n >= 8) {
+        if constexpr (DT == GALE_F32) {
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
+            const uint4 a = q[0], b = q[1];
+            v.u[0] = a.x; v.u[1] = a.y; v.u[2] = a.z; v.u[3] = a.w;
+            v.u[4] = b.x; v.u[5] = b.y; v.u[6] = b.z; v.u[7] = b.w;
         } else {
             const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (dtype == GALE_BF16) {
-                    v[2 * i] = __uint_as_float(w[i] << 16);
-                    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-                } else {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                    v[2 * i] = f.x;
-                    v[2 * i + 1] = f.y;
-                }
-            }
+            v.u[0] = a.x; v.u[1] = a.y; v.u[2] = a.z; v.u[3] = a.w;
         }
+    } else if constexpr (DT == GALE_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v.u[i] = i < n ? static_cast<const uint32_t*>(p)[at + i] : 0u;
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? load_as_f32(p, dtype, at + i) : 0.f;
+        for (int i = 0; i < 4; ++i) {
+            const uint16_t* q = static_cast<const uint16_t*>(p) + at + 2 * i;
+            v.u[i] = (2 * i < n ? uint32_t(q[0]) : 0u) | (2 * i + 1 < n ? uint32_t(q[1]) << 16 : 0u);
+        }
     }
+}
+template <int DT>
+__device__ __forceinline__ void raw8_f32(const Raw8<DT>& r, float (&v)[8]) {
+    if constexpr (DT == GALE_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.u[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (DT == GALE_BF16) {
+                v[2 * i] = __uint_as_float(r.u[i] << 16);
+                v[2 * i + 1] = __uint_as_float(r.u[i] & 0xFFFF0000u);
+            } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.u[i]));
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+    }
+}
+// Calls f with the dtype code and the alignment case as compile-time constants.
+template <typename F>
+inline void by_dtype_vec(int dtype, bool vec, F f) {
+    auto v = [&](auto dt) {
+        if (vec) f(dt, std::true_type());
+        else f(dt, std::false_type());
+    };
+    if (dtype == GALE_F32) v(std::integral_constant<int, GALE_F32>());
+    else if (dtype == GALE_BF16) v(std::integral_constant<int, GALE_BF16>());
+    else v(std::integral_constant<int, GALE_F16>());
 }
 
 // One value rounded to nearest even into dtype (NaN and infinities kept).

@@ -5,7 +5,15 @@
 // kernel is bound by HBM (by latency for a few tokens).  h enters the norm in
 // fp32, before its rounding to the residual's type.  y leaves in 16 or 32 bits
 // and / or as MXFP8 (e4m3 codes, one power-of-two scale per 32 columns).
+//
+// Three kernels: up to 256 columns a warp per row; beyond, a CTA per row, whose
+// rows arrive by bulk copies in a ring of shared-memory stages (registers alone
+// do not hold enough rows in flight: 31 us against the ring's time at 4096 x
+// 4096 in 16 bits); rows too wide for the ring, or not aligned for it, straight
+// into registers.
 #include "mx.cuh"
+#include "ptx.cuh"
+#include "tma.cuh"
 
 namespace gale {
 namespace {
@@ -24,6 +32,8 @@ struct NormArgs {
     int cols, span;      // span: columns written (the padded ones with MXFP8)
     int dt, wt, yt;
     int vw;              // w may be read 16 bytes at a time
+    float inv_cols;
+    int stages, stage_bytes, r_off;      // ring: stages, bytes of one, where the residual's row starts in it
     float eps;
 };
 
@@ -55,13 +65,53 @@ __device__ __forceinline__ void mx8_store_scalar(const NormArgs& a, int64_t row,
     if ((threadIdx.x & 31) == 0) a.s[mx_scale_at(row, c / kMxBlock, a.nt)] = uint8_t(b);
 }
 
+// Eight columns' worth of a row as loaded.  VEC: from column c; otherwise the
+// single elements c + i * threads.
+template <int DT, bool VEC>
+__device__ __forceinline__ void norm_load(const void* p, int64_t at, int cols, int c, int threads, Raw8<DT>& v) {
+    if constexpr (VEC) {
+        load_raw8<DT, true>(p, at + c, cols - c, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = c + i * threads;
+            if constexpr (DT == GALE_F32) {
+                v.u[i] = e < cols ? static_cast<const uint32_t*>(p)[at + e] : 0u;
+            } else {
+                const uint32_t h = e < cols ? uint32_t(static_cast<const uint16_t*>(p)[at + e]) : 0u;
+                v.u[i / 2] = i % 2 ? v.u[i / 2] | h << 16 : h;
+            }
+        }
+    }
+}
+
+// The weights of columns c .. c + 7, `lo` to `n` - 1 of which exist.
+__device__ __forceinline__ void norm_weights(const NormArgs& a, int c, int lo, int n, float (&w)[8]) {
+    if (a.wt == GALE_F32 && a.vw && lo == 0 && n >= 8 && (c & 3) == 0) {
+        Raw8<GALE_F32> u;
+        load_raw8<GALE_F32, true>(a.w, c, 8, u);
+        raw8_f32<GALE_F32>(u, w);
+    } else if (a.wt == GALE_F32 && a.vw && c >= 4 && c + 12 <= a.cols) {
+        // eight of the twelve from the 16-byte boundary before
+        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(a.w) + (c & ~3));
+        const float4 f0 = q[0], f1 = q[1], f2 = q[2];
+        const float f[12] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w, f2.x, f2.y, f2.z, f2.w};
+        const int sh = c & 3;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = sh == 0 ? f[i] : sh == 1 ? f[i + 1] : sh == 2 ? f[i + 2] : f[i + 3];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = i >= lo && i < n ? load_as_f32(a.w, a.wt, c + i) : 0.f;
+    }
+}
+
 // A row per group of `threads` threads (a warp, or the CTA), CH * 8 columns per
 // thread.  VEC: thread t holds columns (j * threads + t) * 8 + i, read and
 // written 16 bytes at a time; otherwise (j * 8 + i) * threads + t, single
 // elements, for rows that are not 16-byte aligned.
-template <bool VEC, int CH, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(NormArgs a) {
-    __shared__ float part[32];
+template <int DT, bool VEC, int CH, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : 512) rmsnorm_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float part[16];
     const int lane = threadIdx.x & 31;
     const int threads = WARP ? 32 : blockDim.x;
     const int t = WARP ? lane : threadIdx.x;
@@ -69,33 +119,20 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(NormArgs a) 
     if (row >= a.tokens) return;      // whole warps (a CTA always has its row)
     float h[CH][8];
     float ss = 0.f;
+    const int stride = VEC ? threads * 8 : threads;      // between a thread's columns j and j + 1 (VEC) / elements
+    Raw8<DT> x[CH];
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-        if constexpr (VEC) {
-            const int c = (j * threads + t) * 8;
-            load8(a.x, a.dt, row * a.ldx + c, a.cols - c, true, h[j]);
-        } else {
+    for (int j = 0; j < CH; ++j)
+        norm_load<DT, VEC>(a.x, row * a.ldx, a.cols, VEC ? j * stride + t * 8 : j * 8 * stride + t, threads, x[j]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int c = (j * 8 + i) * threads + t;
-                h[j][i] = c < a.cols ? load_as_f32(a.x, a.dt, row * a.ldx + c) : 0.f;
-            }
-        }
-    }
+    for (int j = 0; j < CH; ++j) raw8_f32<DT>(x[j], h[j]);
     if (a.r) {
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
+            Raw8<DT> raw;
             float r[8];
-            if constexpr (VEC) {
-                const int c = (j * threads + t) * 8;
-                load8(a.r, a.dt, row * a.ldr + c, a.cols - c, true, r);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int c = (j * 8 + i) * threads + t;
-                    r[i] = c < a.cols ? load_as_f32(a.r, a.dt, row * a.ldr + c) : 0.f;
-                }
-            }
+            norm_load<DT, VEC>(a.r, row * a.ldr, a.cols, VEC ? j * stride + t * 8 : j * 8 * stride + t, threads, raw);
+            raw8_f32<DT>(raw, r);
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[j][i] += r[i];
         }
@@ -110,15 +147,15 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(NormArgs a) 
         __syncthreads();
         ss = warp_sum(lane < (threads >> 5) ? part[lane] : 0.f);
     }
-    const float inv = 1.0f / sqrtf(ss / float(a.cols) + a.eps);
+    const float inv = rsqrtf(fmaf(ss, a.inv_cols, a.eps));
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
         if constexpr (VEC) {
-            const int c = (j * threads + t) * 8;
+            const int c = j * stride + t * 8;
             const int n = a.cols - c;
-            if (a.h && n > 0) store8(a.h, a.dt, row * a.ldh + c, n, true, h[j]);
             float w[8];
-            if (a.w) load8(a.w, a.wt, c, n, a.vw, w);
+            if (a.w) norm_weights(a, c, 0, n, w);
+            if (a.h && n > 0) store8(a.h, DT, row * a.ldh + c, n, true, h[j]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float y = h[j][i] * inv;
@@ -131,7 +168,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(NormArgs a) 
             for (int i = 0; i < 8; ++i) {
                 const int c = (j * 8 + i) * threads + t;
                 const bool in = c < a.cols;
-                if (a.h && in) store_rn(a.h, a.dt, row * a.ldh + c, h[j][i]);
+                if (a.h && in) store_rn(a.h, DT, row * a.ldh + c, h[j][i]);
                 float y = in ? h[j][i] * inv : 0.f;
                 if (a.w && in) y *= load_as_f32(a.w, a.wt, c);
                 if (a.y && in) store_rn(a.y, a.yt, row * a.ldy + c, y);
@@ -141,26 +178,209 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) rmsnorm_kernel(NormArgs a) 
     }
 }
 
+// h of the columns c .. c + 7 straight from the row, 0 outside it.
+template <int DT>
+__device__ __forceinline__ void ring_edge(const NormArgs& a, int64_t row, int c, float (&h)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int e = c + i;
+        float v = 0.f;
+        if (e >= 0 && e < a.cols) {
+            v = load_as_f32(a.x, DT, row * a.ldx + e);
+            if (a.r) v += load_as_f32(a.r, DT, row * a.ldr + e);
+        }
+        h[i] = v;
+    }
+}
+
+// A CTA per row, rows blockIdx.x, + gridDim.x, ...: thread 0 keeps the next
+// `stages` rows' bulk copies in flight.  Rows whose length is no multiple of
+// eight start at any element; every tensor's row starts at the same element
+// modulo 8 (`phase`), so chunks of eight that are aligned in one are in all: a
+// copy takes the aligned bytes around its row (inside the tensor for every row
+// but the last, whose last chunk is read directly), and the first and the last
+// chunk hold columns of the neighbouring rows, which are masked.
+//
+// The weights are in registers before a row's stores are issued (for all rows at
+// once where the rows' phase is always 0): a load behind the stores waited
+// thousands of cycles in the saturated memory pipeline.
+template <int DT, int CH, bool PHASED>
+__global__ void __launch_bounds__(512) rmsnorm_ring_kernel(const __grid_constant__ NormArgs a) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float part[2][16];
+    __shared__ uint64_t full[8];
+    constexpr int ES = DT == GALE_F32 ? 4 : 2;
+    const int lane = threadIdx.x & 31, t = threadIdx.x, threads = blockDim.x;
+    if (t == 0) {
+        for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    auto phase_of = [&](int64_t row) { return PHASED ? int((row * a.ldx) & 7) : 0; };
+    float w[CH][8];
+    auto load_w = [&](int ph) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const int c = (j * threads + t) * 8 - ph;
+            if (a.w) {
+                norm_weights(a, c, c < 0 ? -c : 0, a.cols - c, w[j]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[j][i] = 1.0f;
+            }
+        }
+    };
+    if (!PHASED) load_w(0);
+    auto issue = [&](int64_t row, int s) {
+        const int ph = phase_of(row);
+        int bytes = ((ph + a.cols) * ES + 15) & ~15;
+        if (row + 1 == a.tokens) bytes = (ph + a.cols) * ES & ~15;
+        uint8_t* st = ring + s * a.stage_bytes;
+        mbar_arrive_expect_tx(&full[s], a.r ? 2 * bytes : bytes);
+        if (bytes) {
+            bulk_load(st, static_cast<const uint8_t*>(a.x) + (row * a.ldx - ph) * ES, bytes, &full[s]);
+            if (a.r) bulk_load(st + a.r_off, static_cast<const uint8_t*>(a.r) + (row * a.ldr - ph) * ES, bytes, &full[s]);
+        }
+    };
+    if (t == 0)
+        for (int s = 0; s < a.stages; ++s) {
+            const int64_t row = blockIdx.x + int64_t(s) * gridDim.x;
+            if (row < a.tokens) issue(row, s);
+        }
+    int s = 0, turn = 0;
+    uint32_t parity = 0;
+    for (int64_t row = blockIdx.x; row < a.tokens; row += gridDim.x) {
+        const bool here = mbar_wait_cycles(&full[s], parity);
+        const int ph = phase_of(row);
+        const int have = row + 1 == a.tokens ? (ph + a.cols) * ES / 16 * (16 / ES) - ph : INT32_MAX;   // columns copied
+        const uint8_t* st = ring + s * a.stage_bytes;
+        float h[CH][8];
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const int k = j * threads + t;
+            const int c = k * 8 - ph;
+            if (c < a.cols && c + 8 <= have) {
+                Raw8<DT> x;
+                load_raw8<DT, true>(st, k * 8, 8, x);
+                raw8_f32<DT>(x, h[j]);
+                if (a.r) {
+                    float r[8];
+                    load_raw8<DT, true>(st + a.r_off, k * 8, 8, x);
+                    raw8_f32<DT>(x, r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[j][i] += r[i];
+                }
+                if (c < 0 || c + 8 > a.cols) {      // columns that are not the row's
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[j][i] = c + i >= 0 && c + i < a.cols ? h[j][i] : 0.f;
+                }
+            } else {
+                ring_edge<DT>(a, row, c, h[j]);
+            }
+            if (!here) h[j][0] = __uint_as_float(0x7FC00000u);      // the bounded wait ran out: the row is NaN
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(h[j][i], h[j][i], ss);
+        }
+        if (PHASED) load_w(ph);
+        ss = warp_sum(ss);
+        // (two buffers: a fast warp's next row does not reach into a slow one's read)
+        if (lane == 0) part[turn][t >> 5] = ss;
+        __syncthreads();
+        if (t == 0) {      // every thread has its row in registers: the stage is free
+            const int64_t ahead = row + int64_t(a.stages) * gridDim.x;
+            if (ahead < a.tokens) issue(ahead, s);
+        }
+        ss = warp_sum(lane < (threads >> 5) ? part[turn][lane] : 0.f);
+        turn ^= 1;
+        if (++s == a.stages) {
+            s = 0;
+            parity ^= 1;
+        }
+        const float inv = rsqrtf(fmaf(ss, a.inv_cols, a.eps));
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const int c = (j * threads + t) * 8 - ph;
+            if (c >= 0 && c + 8 <= a.cols) {
+                if (a.h) store8(a.h, DT, row * a.ldh + c, 8, true, h[j]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * inv * w[j][i];
+                if (a.y) store8(a.y, a.yt, row * a.ldy + c, 8, true, h[j]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (c + i < 0 || c + i >= a.cols) continue;
+                    if (a.h) store_rn(a.h, DT, row * a.ldh + c + i, h[j][i]);
+                    h[j][i] = h[j][i] * inv * w[j][i];
+                    if (a.y) store_rn(a.y, a.yt, row * a.ldy + c + i, h[j][i]);
+                }
+            }
+            if (a.q) mx8_store_vec(a, row, c, h[j], c < a.span);      // (phase 0)
+        }
+    }
+}
+
 constexpr int kNormMaxCols = 32768;
 
-template <bool VEC>
-int launch_norm(const NormArgs& a, cudaStream_t st) {
+// Rows straight into registers.
+template <int DT, bool VEC>
+void launch_norm(const NormArgs& a, cudaStream_t st) {
     const int chunks = (a.span + 7) / 8;             // eight-column chunks of a row
     if (chunks <= 128) {                             // up to 1024 columns: a warp per row, eight rows per CTA
         const unsigned grid = unsigned((a.tokens + 7) / 8);
-        if (chunks <= 32) rmsnorm_kernel<VEC, 1, true><<<grid, 256, 0, st>>>(a);
-        else if (chunks <= 64) rmsnorm_kernel<VEC, 2, true><<<grid, 256, 0, st>>>(a);
-        else rmsnorm_kernel<VEC, 4, true><<<grid, 256, 0, st>>>(a);
+        if (chunks <= 32) rmsnorm_kernel<DT, VEC, 1, true><<<grid, 256, 0, st>>>(a);
+        else if (chunks <= 64) rmsnorm_kernel<DT, VEC, 2, true><<<grid, 256, 0, st>>>(a);
+        else rmsnorm_kernel<DT, VEC, 4, true><<<grid, 256, 0, st>>>(a);
     } else {                                         // a CTA per row
         const unsigned grid = unsigned(a.tokens);
-        const int ch = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
+        const int ch = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8;
         const int threads = ((chunks + ch - 1) / ch + 31) / 32 * 32;
-        if (ch == 1) rmsnorm_kernel<VEC, 1, false><<<grid, threads, 0, st>>>(a);
-        else if (ch == 2) rmsnorm_kernel<VEC, 2, false><<<grid, threads, 0, st>>>(a);
-        else rmsnorm_kernel<VEC, 4, false><<<grid, threads, 0, st>>>(a);
+        if (ch == 1) rmsnorm_kernel<DT, VEC, 1, false><<<grid, threads, 0, st>>>(a);
+        else if (ch == 2) rmsnorm_kernel<DT, VEC, 2, false><<<grid, threads, 0, st>>>(a);
+        else if (ch == 4) rmsnorm_kernel<DT, VEC, 4, false><<<grid, threads, 0, st>>>(a);
+        else rmsnorm_kernel<DT, VEC, 8, false><<<grid, threads, 0, st>>>(a);
     }
-    GALE_LAUNCH_CHECK();
-    return GALE_OK;
+}
+
+// Rows through the ring; false if it does not take them.
+template <int DT>
+int launch_norm_ring(NormArgs& a, cudaStream_t st, bool vec, bool& taken) {
+    const int es = DT == GALE_F32 ? 4 : 2;
+    taken = false;
+    const int chunks = (a.span + 7) / 8 + (a.ldx % 8 ? 1 : 0);
+    const int row_bytes = chunks * 8 * es;
+    a.r_off = row_bytes;
+    a.stage_bytes = a.r ? 2 * row_bytes : row_bytes;
+    // 32 columns per thread: what a row costs every thread (barrier, sums, addresses) weighs least
+    const int ch = chunks <= 256 ? 1 : chunks <= 1024 ? 2 : 4;
+    const int threads = ((chunks + ch - 1) / ch + 31) / 32 * 32;
+    // CTAs of an SM by its registers; at least two stages each
+    constexpr int kRoom = 220 * 1024;
+    int per_sm = (ch == 4 ? 512 : ch == 2 ? 1024 : 1536) / threads;
+    if (per_sm > 8) per_sm = 8;
+    if (per_sm < 1) per_sm = 1;
+    while (per_sm > 1 && kRoom / per_sm < 2 * a.stage_bytes) --per_sm;
+    a.stages = kRoom / per_sm / a.stage_bytes;
+    if (a.stages > 8) a.stages = 8;
+    const int64_t most = int64_t(sm_count()) * per_sm;
+    // (a row per CTA at most: straight into registers, where that can be, starts sooner)
+    if (chunks > 2048 || a.stages < 2 || (vec && a.tokens <= most)) return GALE_OK;
+    taken = true;
+    const unsigned grid = unsigned(a.tokens < most ? a.tokens : most);
+    if (a.tokens <= most) a.stages = 1;
+    const int smem = a.stages * a.stage_bytes;
+    auto go = [&](auto kern) {
+        if (ensure_smem(reinterpret_cast<const void*>(kern), smem) != GALE_OK) return GALE_ERR_CUDA;
+        kern<<<grid, threads, smem, st>>>(a);
+        return GALE_OK;
+    };
+    if (a.ldx % 8)
+        return ch == 1   ? go(rmsnorm_ring_kernel<DT, 1, true>)
+               : ch == 2 ? go(rmsnorm_ring_kernel<DT, 2, true>)
+                         : go(rmsnorm_ring_kernel<DT, 4, true>);
+    return ch == 1   ? go(rmsnorm_ring_kernel<DT, 1, false>)
+           : ch == 2 ? go(rmsnorm_ring_kernel<DT, 2, false>)
+                     : go(rmsnorm_ring_kernel<DT, 4, false>);
 }
 
 }  // namespace
@@ -199,6 +419,7 @@ extern "C" int gale_rmsnorm(const void* x, const void* residual, int dtype, int6
     a.wt = w_dtype;
     a.yt = y_dtype;
     a.eps = eps;
+    a.inv_cols = 1.0f / float(cols);
     if (mx8) {
         gale_mx_layout_t L;
         if (gale_mx8_layout(tokens, cols, &L) != GALE_OK) return GALE_ERR_ARG;
@@ -207,8 +428,26 @@ extern "C" int gale_rmsnorm(const void* x, const void* residual, int dtype, int6
         a.nt = L.cols_padded / kMxTile;
         a.span = int(L.cols_padded);
     }
+    a.vw = weight && aligned(weight, 16);
+    cudaStream_t st = as_stream(stream);
     const bool vec = rows_vec(x, dtype, ldx) && (!residual || rows_vec(residual, dtype, ldr)) &&
                      (!sum_out || rows_vec(sum_out, dtype, ldsum)) && (!y || rows_vec(y, y_dtype, ldy));
-    a.vw = weight && aligned(weight, 16);
-    return vec ? launch_norm<true>(a, as_stream(stream)) : launch_norm<false>(a, as_stream(stream));
+    // bases on 16 bytes and row strides that agree modulo 8 elements: the ring (with MXFP8, whose blocks start
+    // with the row, only if rows start on chunks of eight)
+    auto agrees = [&](const void* p, int64_t ld) { return !p || (aligned(p, 16) && (ld - ldx) % 8 == 0); };
+    if (a.span > 256 && agrees(x, ldx) && agrees(residual, ldr) && agrees(sum_out, ldsum) && agrees(y, ldy) &&
+        (!mx8 || ldx % 8 == 0)) {
+        bool taken = false;
+        const int rc = dtype == GALE_F32    ? launch_norm_ring<GALE_F32>(a, st, vec, taken)
+                       : dtype == GALE_BF16 ? launch_norm_ring<GALE_BF16>(a, st, vec, taken)
+                                            : launch_norm_ring<GALE_F16>(a, st, vec, taken);
+        if (rc != GALE_OK) return rc;
+        if (taken) {
+            GALE_LAUNCH_CHECK();
+            return GALE_OK;
+        }
+    }
+    by_dtype_vec(dtype, vec, [&](auto dt, auto v) { launch_norm<decltype(dt)::value, decltype(v)::value>(a, st); });
+    GALE_LAUNCH_CHECK();
+    return GALE_OK;
 }

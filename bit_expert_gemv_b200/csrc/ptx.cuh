@@ -123,6 +123,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
     return true;
 }
 
+// The same bounded by the SM's cycle counter (about 2 s): a read of the global
+// timer takes some 500 cycles, which a ring that turns every few hundred cannot
+// afford.
+__device__ __forceinline__ bool mbar_wait_cycles(uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity))
+        if (clock64() - t0 > 4000000000ll) return false;
+    return true;
+}
+
 // 3-D tiled TMA load into shared memory, completing on `bar` (no multicast).
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
                                             int c2) {

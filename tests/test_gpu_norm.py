@@ -125,13 +125,45 @@ def test_norm_zero_nan_and_inf_rows(cols):
     _close(y[rows], M.rmsnorm(x[rows].double().cpu().numpy())[1], "f32")
 
 
-def test_norm_many_rows_of_every_width():
-    # more rows than CTAs in flight, a warp per row and a CTA per row
-    for cols in (40, 700, 2000):
-        x = _rand((5000, cols), cols, "bf16")
-        y = torch.empty_like(x)
-        G.gale_rmsnorm(x, y=y)
-        _close(y, M.rmsnorm(x.double().cpu().numpy())[1], "bf16")
+@pytest.mark.parametrize("cols", [40, 257, 700, 1001, 2000, 4093, 5001])
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f32", "f32"), ("f16", "f16")])
+def test_norm_many_rows_of_every_width(cols, dtype, out):
+    # more rows than CTAs in flight: every kernel, rows that start at every element modulo 8
+    tokens = 3001
+    x, r = _rand((tokens, cols), cols, dtype), _rand((tokens, cols), cols + 1, dtype)
+    w = 1 + 0.1 * _rand((cols,), 3, "f32")
+    y, h = torch.empty(tokens, cols, dtype=DT[out], device="cuda"), torch.empty_like(x)
+    G.gale_rmsnorm(x, y=y, residual=r, weight=w, sum_out=h)
+    hw, yw = M.rmsnorm(x.double().cpu().numpy(), r.double().cpu().numpy(), w.double().cpu().numpy())
+    _close(y, yw, out)
+    _close(h, hw, dtype)
+    # without the residual, in place
+    G.gale_rmsnorm(x, y=x, weight=w)
+    # (the rows are the inputs' own buffer)
+    _, yw = M.rmsnorm(_rand((tokens, cols), cols, dtype).double().cpu().numpy(), None, w.double().cpu().numpy())
+    _close(x, yw, dtype)
+
+
+@pytest.mark.parametrize("cols,ldx,ldr,ldy", [(1000, 1003, 1011, 1019), (1000, 1001, 1001, 1002), (700, 704, 712, 720),
+                                              (513, 513, 521, 513)])
+def test_norm_many_strided_rows(cols, ldx, ldr, ldy):
+    # strides that agree modulo 8 (the ring) and ones that do not
+    tokens = 2500
+    x, r = _rand((tokens, ldx), 1, "bf16"), _rand((tokens, ldr), 2, "bf16")
+    y = torch.full((tokens, ldy), 5.0, device="cuda", dtype=torch.bfloat16)
+    G.gale_rmsnorm(x[:, :cols], y=y[:, :cols], residual=r[:, :cols])
+    _close(y[:, :cols], M.rmsnorm(x[:, :cols].double().cpu().numpy(), r[:, :cols].double().cpu().numpy())[1], "bf16")
+    assert (y[:, cols:] == 5).all()
+
+
+def test_norm_many_rows_mx8():
+    for cols in (300, 1000, 4000):
+        x, r = _rand((2000, cols), cols, "bf16"), _rand((2000, cols), 7, "bf16")
+        m = torch.empty(G.gale_mx8_layout(2000, cols).total, dtype=torch.uint8, device="cuda")
+        G.gale_rmsnorm(x, mx8=m, residual=r, sum_out=r)
+        hw = x.double().cpu().numpy() + _rand((2000, cols), 7, "bf16").double().cpu().numpy()
+        _close(r, hw, "bf16")
+        _close_mx8(m, M.rmsnorm(hw)[1], 2000, cols)
 
 
 def test_norm_graph_on_another_stream():
