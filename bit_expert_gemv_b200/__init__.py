@@ -312,6 +312,8 @@ def _rows2(t, shape, where: str):
     """Row stride in elements of a [rows, cols] tensor of this shape whose rows are contiguous."""
     if t.shape != shape:
         raise GaleError(GALE_ERR_ARG, where + " (a tensor of another shape)")
+    if t.is_contiguous():
+        return shape[1]
     ld, one = t.stride()
     if one != 1 and shape[1] > 1:
         raise GaleError(GALE_ERR_ARG, where + " (rows must be contiguous)")

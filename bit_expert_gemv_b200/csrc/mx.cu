@@ -5,6 +5,7 @@
 // as plain rows.  The scales of both sit in 512-byte atoms per 128 x 128 tile,
 // in the byte order in which the tensor core's scale columns take them.
 #include "mx.cuh"
+#include "ptx.cuh"
 
 namespace gale {
 namespace {
@@ -90,6 +91,7 @@ template <int DT, bool VEC>
 __global__ void __launch_bounds__(256) mx8_quantize_kernel(const void* __restrict__ x, int64_t ld, int64_t tokens,
                                                            int64_t cols, uint8_t* __restrict__ q,
                                                            uint8_t* __restrict__ s) {
+    pdl_launch_dependents();      // a product behind this kernel may set itself up meanwhile
     const int64_t nt = (cols + kMxTile - 1) / kMxTile;
     const int64_t ct = blockIdx.x % nt;
     const int64_t r0 = blockIdx.x / nt * (16 * kQ8Passes);

@@ -21,6 +21,10 @@
 // half of the tokens' bytes, so a CTA's shared memory takes in 24 KB instead of
 // 40 KB per 128 x 128 x 256 products; the first CTA issues for both.
 //
+// RESIDENT (up to 128 tokens, rows up to 8192 columns): the tokens' scales of all
+// the CTA's columns are copied to TMEM once.  Copying them with every stage cost
+// the issuing warp 14 % at one token, where its instructions set the pace.
+//
 // Without PAIR, the tiles that are left after whole rounds are split over the
 // columns by a cluster of up to 8 CTAs, whose partial sums are added through
 // distributed shared memory in rank order.
@@ -58,6 +62,8 @@ struct GemmArgs {
     int joint;              // left-over tiles of a cluster, at most
     int stages;
     int stage_bytes;
+    int res_off;            // RESIDENT: the tokens' scales in shared memory
+    int res_col;            // and in TMEM
     int cols;               // TMEM columns
     int d1;                 // TMEM column of the second accumulator buffer
     int ydtype;
@@ -91,6 +97,18 @@ __device__ __forceinline__ bool gemm_unit(const GemmArgs& a, int u, GemmUnit& w)
     w.rt = tile / a.ntt;
     w.tt = tile % a.ntt;
     return true;
+}
+
+// The column tiles that this CTA's units cover.
+template <bool PAIR>
+__device__ __forceinline__ void gemm_columns(const GemmArgs& a, int& k0, int& k1) {
+    k0 = 0;
+    k1 = a.nt;
+    GemmUnit w;
+    if (a.whole == 0 && gemm_unit<PAIR>(a, 0, w)) {
+        k0 = w.k0;
+        k1 = w.k1;
+    }
 }
 
 // 16 tokens of one row per lane to y; `full`: all of the warp's rows exist.
@@ -175,7 +193,7 @@ __device__ __forceinline__ void gemm_join(const GemmArgs& a, const GemmUnit& w, 
     }
 }
 
-template <bool PAIR>
+template <bool PAIR, bool RESIDENT>
 __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_constant__ CUtensorMap wmap,
                                                               const __grid_constant__ CUtensorMap xmap,
                                                               const __grid_constant__ GemmArgs a) {
@@ -184,7 +202,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
     // full: a stage's bytes are here (two producers); peer: they are in the pair's other CTA too;
     // empty: its MMAs are done; acc_full: a unit's accumulators are final; acc_free: the columns that
     // the next unit's buffer shares with them have been read
-    __shared__ uint64_t full[kGMaxStages], peer[PAIR ? kGMaxStages : 1], empty[kGMaxStages], acc_full[2], acc_free;
+    __shared__ uint64_t full[kGMaxStages], peer[PAIR ? kGMaxStages : 1], empty[kGMaxStages], acc_full[2], acc_free, res_full;
     __shared__ uint32_t tmem_base;
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     const int rank = PAIR ? int(blockIdx.x & 1) : 0;
@@ -197,6 +215,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
         mbar_init(&acc_full[0], 1);
         mbar_init(&acc_full[1], 1);
         mbar_init(&acc_free, PAIR ? 8 : 4);
+        if (RESIDENT) mbar_init(&res_full, 1);
         fence_mbar_init();
     }
     if (warp == 3) {
@@ -216,6 +235,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
     __syncthreads();
     if (PAIR) cluster_sync();      // the other CTA's barriers are ready too
     tc_fence_after();
+    pdl_wait();                    // the kernels before this one are done: from here on memory is read and written
     const uint32_t tmem = tmem_base;
     const int xrows = PAIR ? a.n / 2 : a.n;      // tokens whose bytes this CTA holds
     const int xbytes = xrows * kMxTile;
@@ -229,10 +249,17 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
         // (st, s8: the stage's shared memory and the offset of its barriers)
         uint32_t st = ring, s8 = 0, phase = 1;      // of the empty barriers: the first turn of the ring passes
         const int atoms_all = int((a.tokens + kMxTile - 1) / kMxTile);
+        if (RESIDENT && warp == 2) {
+            int k0, k1;
+            gemm_columns<PAIR>(a, k0, k1);
+            mbar_expect_lead(lead, smem_u32(&res_full), (k1 - k0) * kMxAtomBytes);
+            bulk_load_lead(lead, ring + a.res_off, a.xsc + int64_t(k0) * kMxAtomBytes, (k1 - k0) * kMxAtomBytes,
+                           smem_u32(&res_full));
+        }
         for (int u = 0; ok && gemm_unit<PAIR>(a, u, w); ++u) {
             const int t0 = w.tt * a.n;
             const int atom0 = t0 / kMxTile;
-            const int atoms = min(a.xatoms, atoms_all - atom0);
+            const int atoms = RESIDENT ? 0 : min(a.xatoms, atoms_all - atom0);
             const int rt = PAIR ? 2 * w.rt + rank : w.rt;
             // (a pair's second row tile may not exist: its lines read as zero, its scales are the last tile's)
             const uint8_t* wsc = a.wsc + int64_t(min(rt, a.rtiles - 1)) * a.nt * kMxAtomBytes;
@@ -278,6 +305,20 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
         const uint32_t idesc = umma_idesc_mx(PAIR ? 2 * kMxTile : kMxTile, a.n);
         const uint32_t sf_first = tmem + a.cols - a.stages * a.sfcols;
         const uint64_t xstep = xbytes >> 4;
+        int kres = 0;
+        if (RESIDENT) {
+            int k1;
+            gemm_columns<PAIR>(a, kres, k1);
+            ok = mbar_wait_warp(smem_u32(&res_full), 0);
+            if (ok) {
+                tc_fence_after();
+                for (int k = kres; k < k1; ++k)
+                    tmem_copy_scales(lead, tmem + a.res_col + 4 * (k - kres),
+                                     scale_atom_desc(ring + a.res_off + (k - kres) * kMxAtomBytes));
+            }
+        }
+        // scale copies of a stage, and their TMEM columns per column tile
+        const int ncopy = RESIDENT ? 1 : 1 + a.xatoms;
         uint32_t st = ring, s8 = 0, phase = 0, sf = sf_first;
         for (int u = 0; ok && gemm_unit<PAIR>(a, u, w); ++u) {
             const uint32_t d = tmem + ((u & 1) ? a.d1 : 0);
@@ -297,8 +338,8 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
 #pragma unroll
                 for (int j = 0; j < kGK; ++j) {
                     if (j == kt) break;
-                    const uint32_t sfj = sf + j * 4 * (1 + a.xatoms);
-                    for (int i = 0; i <= a.xatoms; ++i) {
+                    const uint32_t sfj = sf + j * 4 * ncopy;
+                    for (int i = 0; i < ncopy; ++i) {
                         if (PAIR) tmem_copy_scales_pair(lead, sfj + 4 * i, from + (i * kGK + j) * (kMxAtomBytes >> 4));
                         else tmem_copy_scales(lead, sfj + 4 * i, from + (i * kGK + j) * (kMxAtomBytes >> 4));
                     }
@@ -306,14 +347,15 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
 #pragma unroll
                 for (int j = 0; j < kGK; ++j) {
                     if (j == kt) break;
-                    const uint32_t sfj = sf + j * 4 * (1 + a.xatoms);
+                    const uint32_t sfj = sf + j * 4 * ncopy;
+                    const uint32_t sfx = RESIDENT ? tmem + a.res_col + 4 * (k + j - kres) : sfj + xoff;
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
                         const uint32_t more = (k > w.k0 || j > 0 || b > 0) ? 1u : 0u;
                         const uint32_t id = umma_idesc_scale_id(idesc, b);
                         const uint64_t aj = ad + j * (kGABytes >> 4) + 2 * b, bj = bd + j * xstep + 2 * b;
-                        if (PAIR) umma_mx_pair(lead, d, aj, bj, id, sfj, sfj + xoff, more);
-                        else umma_mx(lead, d, aj, bj, id, sfj, sfj + xoff, more);
+                        if (PAIR) umma_mx_pair(lead, d, aj, bj, id, sfj, sfx, more);
+                        else umma_mx(lead, d, aj, bj, id, sfj, sfx, more);
                     }
                 }
                 if (PAIR) umma_commit_pair(lead, &empty[0] + (s8 >> 3));
@@ -427,7 +469,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
 
 struct GemmPlan {
     GemmArgs a;
-    bool pair;
+    bool pair, resident;
     int grid, smem;
 };
 
@@ -448,7 +490,7 @@ int gemm_clusters(int size) {
     const int slot = size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : 3;
     if (!found[dev][slot]) {
         int n = 0;
-        if (ensure_smem(reinterpret_cast<const void*>(mx_gemm_kernel<false>), kGSmemSm) != GALE_OK) return 0;
+        if (ensure_smem(reinterpret_cast<const void*>(mx_gemm_kernel<false, false>), kGSmemSm) != GALE_OK) return 0;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(unsigned(size) * 16);
         cfg.blockDim = dim3(kGThreads);
@@ -458,7 +500,7 @@ int gemm_clusters(int size) {
         at[0].val.clusterDim = {unsigned(size), 1, 1};
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, mx_gemm_kernel<false>, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&n, mx_gemm_kernel<false, false>, &cfg) != cudaSuccess) {
             cudaGetLastError();
             return 0;
         }
@@ -519,17 +561,23 @@ bool gemm_plan(int64_t rows, int nt, int64_t tokens, GemmPlan& p) {
         p.grid = a.workers;
     }
     const int xrows = p.pair ? a.n / 2 : a.n;
-    a.stage_bytes = int(align_up(kGK * (kGABytes + xrows * kMxTile + kMxAtomBytes * (1 + a.xatoms)), 1024));
-    a.stages = (kGSmemSm - 1024 - join_bytes) / a.stage_bytes;
+    p.resident = !p.pair && a.ntt == 1 && a.xatoms == 1 && nt <= 64;
+    const int ncopy = p.resident ? 1 : 1 + a.xatoms;
+    const int res_bytes = p.resident ? int(align_up((a.whole ? nt : (nt + a.split - 1) / a.split + kGK) * kMxAtomBytes, 1024)) : 0;
+    a.stage_bytes = int(align_up(kGK * (kGABytes + xrows * kMxTile + kMxAtomBytes * ncopy), 1024));
+    a.stages = (kGSmemSm - 1024 - join_bytes - res_bytes) / a.stage_bytes;
     if (a.stages > kGMaxStages) a.stages = kGMaxStages;
-    a.sfcols = kGK * 4 * (1 + a.xatoms);
+    a.res_off = a.stages * a.stage_bytes + join_bytes;
+    a.sfcols = kGK * 4 * ncopy;
+    const int res_cols = p.resident ? 4 * nt : 0;
     const int units = a.whole + a.joint;
     int cols = 32;
-    while (cols < (units > 1 ? 2 : 1) * a.n + a.stages * a.sfcols && cols < 512) cols *= 2;
+    while (cols < (units > 1 ? 2 : 1) * a.n + a.stages * a.sfcols + res_cols && cols < 512) cols *= 2;
     a.cols = cols;
-    const int avail = (cols - a.stages * a.sfcols) / 16 * 16;
+    const int avail = (cols - a.stages * a.sfcols - res_cols) / 16 * 16;
     a.d1 = units == 1 || avail >= 2 * a.n ? a.n : avail - a.n;
-    p.smem = a.stages * a.stage_bytes + join_bytes + 1024;
+    a.res_col = cols - a.stages * a.sfcols - res_cols;
+    p.smem = a.stages * a.stage_bytes + join_bytes + res_bytes + 1024;
     // As large a share of the SM's shared memory as of its TMEM, so that a CTA
     // that is resident never waits for TMEM columns.
     const int least = int(int64_t(kGSmemSm) * cols / 512);
@@ -572,18 +620,21 @@ extern "C" int gale_mx_gemm(const void* w4, int64_t rows, int64_t cols, const vo
     if (rc == GALE_OK) rc = make_map_bytes(&xmap, x, W.cols_padded, tokens, kMxTile, p.pair ? p.a.n / 2 : p.a.n);
     if (rc != GALE_OK) return rc;
     p.a.pair16 = ldy % 2 == 0 && aligned(y, 4);
-    auto kern = p.pair ? mx_gemm_kernel<true> : mx_gemm_kernel<false>;
+    auto kern = p.pair ? mx_gemm_kernel<true, false> : p.resident ? mx_gemm_kernel<false, true> : mx_gemm_kernel<false, false>;
     if (ensure_smem(reinterpret_cast<const void*>(kern), p.smem) != GALE_OK) return GALE_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(p.grid));
     cfg.blockDim = dim3(kGThreads);
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = as_stream(stream);
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim = {unsigned(p.pair ? 2 : p.a.split), 1, 1};
+    // its set-up may run while the kernel before it ends (the kernel waits for that before it touches memory)
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, kern, wmap, xmap, p.a) != cudaSuccess) {
         cudaGetLastError();      // reported here, not by the next call
         return GALE_ERR_CUDA;

@@ -112,6 +112,7 @@ __device__ __forceinline__ void norm_weights(const NormArgs& a, int c, int lo, i
 template <int DT, bool VEC, int CH, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : 512) rmsnorm_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float part[16];
+    if (a.q) pdl_launch_dependents();      // a product behind this kernel may set itself up meanwhile
     const int lane = threadIdx.x & 31;
     const int threads = WARP ? 32 : blockDim.x;
     const int t = WARP ? lane : threadIdx.x;
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(512) rmsnorm_ring_kernel(const __grid_constant
     __shared__ float part[2][16];
     __shared__ uint64_t full[8];
     constexpr int ES = DT == GALE_F32 ? 4 : 2;
+    if (a.q) pdl_launch_dependents();
     const int lane = threadIdx.x & 31, t = threadIdx.x, threads = blockDim.x;
     if (t == 0) {
         for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1);
