@@ -139,6 +139,41 @@ __device__ __forceinline__ uint32_t kept_groups(const SelectArgs& a, T score, in
     return __ballot_sync(0xffffffffu, lane < a.groups && rank < a.keep);
 }
 
+// The two largest keys of every group, from a warp's keys in shared memory (a pad
+// word per 32 against bank conflicts): 2^lanes_log2 neighbouring lanes read a
+// group; lane g returns group g's (-inf where there is none, or none asked for).
+template <typename T>
+__device__ __forceinline__ void group_best(const SelectArgs& a, const T* keys, int lane, T& m1, T& m2) {
+    const int lg = a.lanes_log2, L = 1 << lg;
+    const int g = lane >> lg;
+    m1 = m2 = T(-INFINITY);
+    if (g < a.groups) {
+        for (int i = lane & (L - 1); i < a.gsize; i += L) {
+            const int e = g * a.gsize + i;
+            const T v = keys[e + (e >> 5)], low = m1 < v ? m1 : v;
+            m2 = m2 > low ? m2 : low;
+            m1 = m1 > v ? m1 : v;
+        }
+    }
+    for (int o = 1; o < L; o <<= 1) {
+        const T u1 = __shfl_xor_sync(0xffffffffu, m1, o), u2 = __shfl_xor_sync(0xffffffffu, m2, o);
+        const T low = m1 < u1 ? m1 : u1;
+        m2 = m2 > u2 ? m2 : u2;
+        m2 = m2 > low ? m2 : low;
+        m1 = m1 > u1 ? m1 : u1;
+    }
+    m1 = __shfl_sync(0xffffffffu, m1, (lane << lg) & 31);
+    m2 = __shfl_sync(0xffffffffu, m2, (lane << lg) & 31);
+    if (lane >= a.groups) m1 = m2 = T(-INFINITY);
+    if (a.gtop == 1) m2 = T(-INFINITY);
+}
+// Their sum, of those that are there.
+template <typename T>
+__device__ __forceinline__ T group_sum(T m1, T m2) {
+    const T score = m2 > T(-INFINITY) ? m1 + m2 : m1;
+    return score == score ? score : T(-INFINITY);
+}
+
 // The whole selection in 64 bits; lane k < K returns pick k.
 template <int V>
 __device__ __noinline__ int select_exact(const SelectArgs& a, int64_t t, int lane) {
@@ -203,9 +238,6 @@ __device__ __forceinline__ uint32_t order_bits(float f) {
     const uint32_t u = __float_as_uint(f + 0.0f);
     return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float order_value(uint32_t o) {
-    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
-}
 
 // Whether a >= b is certain to be the order of the 64-bit values when either
 // is known to es + 2^-24 |value|.  Infinities are exact.
@@ -229,62 +261,81 @@ __device__ __forceinline__ double score64(const SelectArgs& a, float l, float lm
     return a.sigmoid ? 1.0 / (1.0 + exp(-double(l))) : sum > 0.0 ? exp(double(l) - double(lmax)) / sum : 0.0;
 }
 
-// Sorts n <= 32 candidates (one per lane, `live`) by descending key, the lower
-// id first: lane r gets the r-th.
-template <typename T>
-__device__ __forceinline__ void sort_lanes(int n, int lane, bool live, T& key, int& id) {
+// The groups that stay with a bias, by 64-bit scores (`keys`: the warp's shared memory).
+template <int V>
+__device__ __noinline__ uint32_t exact_groups(const SelectArgs& a, int64_t t, int lane, float lmax, double* keys) {
+    float l[V];
+    load_logits<V>(a, t, lane, l);
+    const double sum = a.sigmoid ? 1.0 : softmax_sum64<V>(l, lmax);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int e = lane + 32 * j;
+        keys[lane + 33 * j] = with_bias(score64(a, l[j], lmax, sum), e < a.E ? a.bias[e] : 0.f, l[j] == kMinusInf);
+    }
+    __syncwarp();
+    double m1, m2;
+    group_best(a, keys, lane, m1, m2);
+    return kept_groups(a, group_sum(m1, m2), lane);
+}
+
+// Keys with a bias as fixed point below the token's largest one, `hi`: the
+// fraction bits of key + c in [1, 2), c = 1.9999 - hi, keys further down at 1 +
+// 2^-23, masked ones at 1; over a bit that says the expert exists and its index
+// (inverted).  23 bits (two less for many experts) resolve what fp32 keys can
+// tell, where the leading bits of a float resolved 2^-16 and one token in ten had
+// neighbouring picks in doubt.
+template <int V>
+struct Fixed {
+    static constexpr uint32_t kIndex = 32 * V - 1;
+    static constexpr int kLow = V <= 8 ? 9 : V == 16 ? 10 : 11;     // index and existence bits
+    static constexpr float kUnit = 1.1920929e-7f * (1 << (kLow - 9));
+    static __device__ __forceinline__ uint32_t pack(float key, float c, int e) {
+        const float f = key == kMinusInf ? 1.0f : fmaxf(key + c, 1.0000001f);
+        return ((__float_as_uint(f) << 9) & ~((1u << kLow) - 1u)) | (1u << (kLow - 1)) | (kIndex - e);
+    }
+    static __device__ __forceinline__ int expert(uint32_t m) { return int(kIndex - (m & kIndex)); }
+    static __device__ __forceinline__ int fraction(uint32_t m) { return int(m >> kLow); }
+};
+
+// The picks with a bias where the order of the fp32 keys is in doubt: lane i holds
+// the i-th largest of n packed keys, `m` (0: there were no more); sorts them by
+// their 64-bit keys.  False if an expert that is not among them could still
+// belong to the picks.
+template <int V>
+__device__ __noinline__ bool refine(const SelectArgs& a, int64_t t, int lane, int n, float margin, float c, float lmax,
+                                    uint32_t m, int& pick) {
+    using F = Fixed<V>;
+    const bool live = lane < n && m != 0u;
+    const uint32_t last = __shfl_sync(0xffffffffu, m, n - 1);
+    const int id = live ? F::expert(m) : -1;
+    const float l = live ? logit_at(a, t, id) : kMinusInf;
+    const float b = live ? a.bias[id] : 0.f;
+    double sum = 1.0;
+    if (!a.sigmoid) {
+        float all[V];
+        load_logits<V>(a, t, lane, all);
+        sum = softmax_sum64<V>(all, lmax);
+    }
+    const double key = with_bias(score64(a, l, lmax, sum), b, l == kMinusInf);
     int rank = live ? 0 : 32;
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
-        const T o = __shfl_sync(0xffffffffu, key, i);
-        const int oid = __shfl_sync(0xffffffffu, live ? id : -1, i);
+        const double o = __shfl_sync(0xffffffffu, key, i);
+        const int oid = __shfl_sync(0xffffffffu, id, i);
         rank += oid >= 0 && (o > key || (o == key && oid < id));
     }
-    const T k0 = key;
-    const int id0 = id;
+    float kth = 0.f;
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
-        const int r = __shfl_sync(0xffffffffu, rank, i), oid = __shfl_sync(0xffffffffu, id0, i);
-        const T o = __shfl_sync(0xffffffffu, k0, i);
-        if (r == lane) {
-            key = o;
-            id = oid;
-        }
+        const int r = __shfl_sync(0xffffffffu, rank, i), oid = __shfl_sync(0xffffffffu, id, i);
+        const float o = __shfl_sync(0xffffffffu, float(key), i);
+        if (r == lane) pick = oid;
+        if (r == a.K - 1) kth = o;
     }
-}
-
-// Picks with a bias where the packed keys leave their order in doubt: lane i
-// holds the i-th largest of n packed keys, `m` (0: there were no more).  Sorts
-// them by their fp32 keys, and by the 64-bit ones if those are in doubt too.
-// False if an expert that is not among them could still belong to the picks.
-template <int V>
-__device__ __noinline__ bool refine(const SelectArgs& a, int64_t t, int lane, int n, float es, float lmax, float inv,
-                                    uint32_t m, int& id) {
-    constexpr uint32_t kIndex = 32 * V - 1;
-    const bool live = lane < n && m != 0u;
-    const int count = __popc(__ballot_sync(0xffffffffu, live));
-    const uint32_t last = __shfl_sync(0xffffffffu, m, n - 1);
-    const int first = live ? int(kIndex - (m & kIndex)) : 0;
-    const float l = live ? logit_at(a, t, first) : kMinusInf;
-    const float b = live ? a.bias[first] : 0.f;
-    float key = with_bias(score32(a, l, lmax, inv), b, l == kMinusInf);
-    id = first;
-    sort_lanes(n, lane, live, key, id);
-    const float next = __shfl_down_sync(0xffffffffu, key, 1);
-    if (__any_sync(0xffffffffu, lane < a.K && lane + 1 < count && !certain(key, next, es))) {
-        double sum = 1.0;
-        if (!a.sigmoid) {
-            float all[V];
-            load_logits<V>(a, t, lane, all);
-            sum = softmax_sum64<V>(all, lmax);
-        }
-        double exact = with_bias(score64(a, l, lmax, sum), b, l == kMinusInf);
-        id = first;
-        sort_lanes(n, lane, live, exact, id);
-        key = float(exact);
-    }
-    const float kth = __shfl_sync(0xffffffffu, key, a.K - 1);
-    return last == 0u || certain(kth, order_value(last | kIndex), es);
+    // a key that is not among the n is at most the last one's
+    const float most = 1.0f + float(F::fraction(last) + 1) * F::kUnit - c;
+    return last == 0u || F::fraction(last) == 0 || kth - most > margin;
 }
 
 // The sum over lanes 0 .. K - 1 (zeros from K on), valid in those lanes.
@@ -427,13 +478,15 @@ __device__ __forceinline__ uint32_t take_packed(const uint32_t (&pk)[V], int n, 
 // CTAs of 8 warps that an SM is to hold.
 template <int V, bool SCORED>
 constexpr int select_ctas() {
-    return V <= 8 ? (SCORED ? 3 : 5) : V == 16 ? (SCORED ? 2 : 3) : (SCORED ? 1 : 2);
+    return V <= 8 ? (SCORED ? 4 : 5) : V == 16 ? (SCORED ? 2 : 3) : (SCORED ? 1 : 2);
 }
 
 // SCORED: with a bias or groups; otherwise the keys are the logits.
 template <int V, bool SCORED>
 __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_kernel(const __grid_constant__ SelectArgs a) {
-    __shared__ float group_keys[SCORED ? 8 : 1][SCORED ? 33 * V : 1];
+    // (64-bit keys of 1024 experts would not fit: their doubtful groups are left to select_exact)
+    using GroupKey = std::conditional_t<V <= 16, double, float>;
+    __shared__ GroupKey group_keys[SCORED ? 8 : 1][SCORED ? 33 * V : 1];
     constexpr uint32_t kIndex = 32 * V - 1;      // the bits of a packed key that hold the expert
     const int lane = threadIdx.x & 31;
     const int64_t t = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -510,39 +563,18 @@ __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_ke
         uint32_t kept = 0xFFFFFFFFu;
         bool sure = true;
         if (a.groups > 1 && a.keep < a.groups) {
-            // a group's keys to 2^lanes_log2 neighbouring lanes through shared memory (a pad word per 32
-            // against bank conflicts), its two largest to lane g
-            float* gk = group_keys[threadIdx.x >> 5];
+            float* gk = reinterpret_cast<float*>(group_keys[threadIdx.x >> 5]);
 #pragma unroll
             for (int j = 0; j < V; ++j) gk[lane + 33 * j] = s[j];
             __syncwarp();
-            const int lg = a.lanes_log2, L = 1 << lg;
-            const int g = lane >> lg;
-            float m1 = kMinusInf, m2 = kMinusInf;
-            if (g < a.groups) {
-                for (int i = lane & (L - 1); i < a.gsize; i += L) {
-                    const int e = g * a.gsize + i;
-                    const float v = gk[e + (e >> 5)];
-                    m2 = fmaxf(m2, fminf(m1, v));
-                    m1 = fmaxf(m1, v);
-                }
-            }
-            for (int o = 1; o < L; o <<= 1) {
-                const float u1 = __shfl_xor_sync(0xffffffffu, m1, o), u2 = __shfl_xor_sync(0xffffffffu, m2, o);
-                m2 = fmaxf(fmaxf(m2, u2), fminf(m1, u1));
-                m1 = fmaxf(m1, u1);
-            }
-            m1 = __shfl_sync(0xffffffffu, m1, (lane << lg) & 31);
-            m2 = __shfl_sync(0xffffffffu, m2, (lane << lg) & 31);
-            if (lane >= a.groups) m1 = m2 = kMinusInf;
-            if (a.gtop == 1) m2 = kMinusInf;
+            float m1, m2;
+            group_best(a, gk, lane, m1, m2);
             // what a sum of two is off by: twice es, and the roundings of the keys and of the sum
             const float k1 = a.bias || m1 == kMinusInf ? m1 : score32(a, m1, lmax, inv);
             const float k2 = a.bias || m2 == kMinusInf ? m2 : score32(a, m2, lmax, inv);
             const float f1 = fabsf(k1), f2 = fabsf(k2);
             const float big = warp_max_t(fmaxf(f1 < INFINITY ? f1 : 0.f, f2 < INFINITY ? f2 : 0.f));
-            float score = k2 > kMinusInf ? k1 + k2 : k1;
-            if (!(score == score)) score = kMinusInf;
+            const float score = group_sum(k1, k2);
             kept = kept_groups(a, score, lane);
             const bool in = (kept >> lane) & 1u;
             const float worst = -warp_max_t(in ? -score : kMinusInf);
@@ -551,35 +583,57 @@ __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_ke
             if (!sure && !a.bias) {
                 // the best two of a group are certain (by logit): their scores in 64 bits
                 const double all = a.sigmoid ? 1.0 : softmax_sum64<V>(l, lmax);
-                const double d1 = score64(a, m1, lmax, all), d2 = score64(a, m2, lmax, all);
-                kept = kept_groups(a, m1 == kMinusInf ? double(kMinusInf) : m2 == kMinusInf ? d1 : d1 + d2, lane);
+                const double d1 = m1 == kMinusInf ? double(kMinusInf) : score64(a, m1, lmax, all);
+                const double d2 = m2 == kMinusInf ? double(kMinusInf) : score64(a, m2, lmax, all);
+                kept = kept_groups(a, group_sum(d1, d2), lane);
+                sure = true;
+            } else if (!sure && V <= 16) {
+                kept = exact_groups<V>(a, t, lane, lmax, reinterpret_cast<double*>(group_keys[threadIdx.x >> 5]));
                 sure = true;
             }
         }
+        // experts whose group went: 0, below every key
+        auto stays = [&](int e) {
+            return e < a.E && ((kept >> (a.groups > 1 ? int(uint32_t(e) * a.gmagic >> 20) : 0)) & 1u);
+        };
+        if (a.bias) {
+            using F = Fixed<V>;
+            float hi = kMinusInf;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            // an expert whose group went: 0, below every key
-            const int e = lane + 32 * j;
-            const int g = a.groups > 1 ? int(uint32_t(e) * a.gmagic >> 20) : 0;
-            pk[j] = e < a.E && ((kept >> g) & 1u) ? (order_bits(s[j]) & ~kIndex) | (kIndex - e) : 0u;
-        }
-        if (sure) {
-            // one more than is picked: the last pick's lead counts too
+            for (int j = 0; j < V; ++j) hi = stays(lane + 32 * j) ? fmaxf(hi, s[j]) : hi;
+            hi = warp_max_t(hi);
+            sure = sure && hi < INFINITY;
+            if (sure) {
+                const float c = hi == kMinusInf ? 0.f : 1.9999f - hi;
+                // what two keys' difference may be off by: the scores, their roundings with the bias and with c
+                const float margin = 2.0f * es + 2.4e-7f * (fmaxf(fabsf(hi), 0.f) + 2.0f);
+#pragma unroll
+                for (int j = 0; j < V; ++j) pk[j] = stays(lane + 32 * j) ? F::pack(s[j], c, lane + 32 * j) : 0u;
+                // one more than is picked: the last pick's lead counts too
+                const uint32_t m = take_packed<V>(pk, a.K + 1, lane);
+                const uint32_t next = __shfl_down_sync(0xffffffffu, m, 1);
+                id = F::expert(m);
+                const bool clear = lane >= a.K || next == 0u || F::fraction(next) == 0 ||
+                                   float(F::fraction(m) - F::fraction(next) - 1) * F::kUnit > margin;
+                if (!__all_sync(0xffffffffu, clear)) {
+                    const int n = a.K + 3;
+                    const uint32_t mn = take_packed<V>(pk, n, lane);
+                    sure = refine<V>(a, t, lane, n, margin, c, lmax, mn, id);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int e = lane + 32 * j;
+                pk[j] = stays(e) ? (order_bits(s[j]) & ~kIndex) | (kIndex - e) : 0u;
+            }
             const uint32_t m = take_packed<V>(pk, a.K + 1, lane);
             const uint32_t next = __shfl_down_sync(0xffffffffu, m, 1);
             id = int(kIndex - (m & kIndex));
-            if (a.bias) {
-                // m's key is at least, next's at most
-                const float low = order_value(m & ~kIndex), high = order_value(next | kIndex);
-                if (!__all_sync(0xffffffffu, lane >= a.K || next == 0u || certain(low, high, es))) {
-                    const int n = a.K + 8;
-                    const uint32_t mn = take_packed<V>(pk, n, lane);
-                    sure = refine<V>(a, t, lane, n, es, lmax, inv, mn, id);
-                }
-            } else if (a.dtype == GALE_F32 &&
-                       __any_sync(0xffffffffu, lane < a.K && next != 0u && ((m ^ next) & ~kIndex) == 0u)) {
+            if (a.dtype == GALE_F32 &&
+                __any_sync(0xffffffffu, lane < a.K && next != 0u && ((m ^ next) & ~kIndex) == 0u)) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) pk[j] = pk[j] != 0u ? order_bits(l[j]) : 0u;
+                for (int j = 0; j < V; ++j) pk[j] = pk[j] != 0u ? order_bits(s[j]) : 0u;
                 id = take_largest<V>(pk, a.K, lane);
             }
         }
