@@ -45,25 +45,36 @@ __device__ __forceinline__ float logit_at(const SelectArgs& a, int64_t t, int e)
     return clean(load_as_f32(a.logits, a.dtype, t * a.ld + e));
 }
 // The logits of experts lane, lane + 32, ...; -inf past the last.
-template <int V>
-__device__ __forceinline__ void load_logits(const SelectArgs& a, int64_t t, int lane, float (&l)[V]) {
+template <int V, bool FULL>
+__device__ __forceinline__ void load_logits_of(const SelectArgs& a, int64_t t, int lane, float (&l)[V]) {
     if (a.dtype == GALE_F32) {
         const float* p = static_cast<const float*>(a.logits) + t * a.ld + lane;
 #pragma unroll
-        for (int j = 0; j < V; ++j) l[j] = lane + 32 * j < a.E ? __ldg(p + 32 * j) : kMinusInf;
+        for (int j = 0; j < V; ++j) l[j] = FULL || lane + 32 * j < a.E ? __ldg(p + 32 * j) : kMinusInf;
     } else {
         const uint16_t* p = static_cast<const uint16_t*>(a.logits) + t * a.ld + lane;
         uint16_t u[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) u[j] = lane + 32 * j < a.E ? __ldg(p + 32 * j) : 0;
+        for (int j = 0; j < V; ++j) u[j] = FULL || lane + 32 * j < a.E ? __ldg(p + 32 * j) : 0;
+        if (a.dtype == GALE_BF16) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float f = a.dtype == GALE_BF16 ? bf16_to_f32(u[j]) : __half2float(__ushort_as_half(u[j]));
-            l[j] = lane + 32 * j < a.E ? f : kMinusInf;
+            for (int j = 0; j < V; ++j) l[j] = bf16_to_f32(u[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) l[j] = __half2float(__ushort_as_half(u[j]));
+        }
+        if (!FULL) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) l[j] = lane + 32 * j < a.E ? l[j] : kMinusInf;
         }
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) l[j] = clean(l[j]);
+}
+template <int V>
+__device__ __forceinline__ void load_logits(const SelectArgs& a, int64_t t, int lane, float (&l)[V]) {
+    if (a.E == 32 * V) load_logits_of<V, true>(a, t, lane, l);
+    else load_logits_of<V, false>(a, t, lane, l);
 }
 // s + b, -inf for a masked expert or a NaN
 template <typename T>
@@ -431,14 +442,14 @@ __device__ __forceinline__ int take_largest(const uint32_t (&key)[V], int n, int
     return mine;
 }
 
-// A lane's three largest packed keys below `under`.
-template <int V>
+// A lane's three largest packed keys; NEXT: of those below `under`.
+template <int V, bool NEXT>
 __device__ __forceinline__ void lane_top3(const uint32_t (&pk)[V], uint32_t under, uint32_t& h1, uint32_t& h2,
                                           uint32_t& h3) {
     h1 = h2 = h3 = 0u;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        uint32_t k = pk[j] < under ? pk[j] : 0u, low = min(h1, k);
+        uint32_t k = !NEXT || pk[j] < under ? pk[j] : 0u, low = min(h1, k);
         h1 = max(h1, k);
         k = min(h2, low);
         h2 = max(h2, low);
@@ -454,7 +465,7 @@ __device__ __forceinline__ void lane_top3(const uint32_t (&pk)[V], uint32_t unde
 template <int V>
 __device__ __forceinline__ uint32_t take_packed(const uint32_t (&pk)[V], int n, int lane) {
     uint32_t h1, h2, h3, mine = 0u;
-    lane_top3<V>(pk, 0xFFFFFFFFu, h1, h2, h3);
+    lane_top3<V, false>(pk, 0u, h1, h2, h3);
     for (int k = 0; k < n; ++k) {
         const uint32_t m = __reduce_max_sync(0xffffffffu, h1);
         mine = lane == k ? m : mine;
@@ -464,7 +475,7 @@ __device__ __forceinline__ uint32_t take_packed(const uint32_t (&pk)[V], int n, 
         h3 = own ? 0u : h3;
         if (V > 3 && __any_sync(0xffffffffu, own && h1 == 0u)) {
             uint32_t g1, g2, g3;
-            lane_top3<V>(pk, m, g1, g2, g3);
+            lane_top3<V, true>(pk, m, g1, g2, g3);
             if (own) {
                 h1 = g1;
                 h2 = g2;
@@ -508,9 +519,10 @@ __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_ke
             sum = warp_sum(sum);
         }
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int e = lane + 32 * j;
-            pk[j] = e < a.E ? (order_bits(l[j]) & ~kIndex) | (kIndex - e) : 0u;
+        for (int j = 0; j < V; ++j) pk[j] = (order_bits(l[j]) & ~kIndex) | (kIndex - lane - 32 * j);
+        if (a.E < 32 * V) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) pk[j] = lane + 32 * j < a.E ? pk[j] : 0u;
         }
         // 16-bit logits are packed whole; others with one more than is picked, to see a tie of the last
         const bool whole = a.dtype != GALE_F32;
