@@ -1,0 +1,148 @@
+"""The operators around the experts as one block, the way a layer runs them:
+norm of the residual sum (16-bit and 8-bit outputs) -> router product -> router
+by scores -> routed experts -> next norm.  Every step is compared with the fp64
+oracle on the step's own inputs (an expert choice that flips on a rounding
+upstream would say nothing), and the block as a captured graph with the eager
+calls, bit for bit.
+"""
+import numpy as np
+import pytest
+
+import gale_synth as gs
+from oracle import gale_oracle as O
+from oracle import mx_oracle as M
+from oracle import route_oracle as R
+
+from .helpers import Layer, assert_tokens
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+G = pytest.importorskip("bit_expert_gemv_b200")
+
+D, FF, E, K = 2048, 1024, 32, 6
+GROUPS = (8, 4, 2)
+
+
+@pytest.fixture(scope="module")
+def layer():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return Layer(E, D, FF, layer=3)
+
+
+def _normal(shape, tag, scale=1.0):
+    n = int(np.prod(shape))
+    v = gs.normal(gs.stream_key(91, tag), n).astype(np.float32).reshape(shape) * np.float32(scale)
+    return torch.from_numpy(v).cuda()
+
+
+class Block:
+    def __init__(self, layer, T):
+        self.layer, self.T = layer, T
+        self.x = _normal((T, D), 1).bfloat16()
+        self.res = _normal((T, D), 2, 3.0).bfloat16()
+        self.w1, self.w2 = 1 + 0.1 * _normal((D,), 3), (1 + 0.1 * _normal((D,), 4)).bfloat16()
+        self.router = _normal((E, D), 5, 0.02)
+        self.bias = _normal((E,), 6, 0.05)
+        self.w4 = torch.empty(G.gale_mx4_layout(E, D).total, dtype=torch.uint8, device="cuda")
+        G.gale_mx4_quantize(self.router, self.w4)
+        self.h, self.y, self.out, self.h2, self.y2 = (torch.zeros_like(self.x) for _ in range(5))
+        self.x8 = torch.zeros(G.gale_mx8_layout(T, D).total, dtype=torch.uint8, device="cuda")
+        self.logits = torch.zeros(T, E, device="cuda")
+        self.gemm_ws = torch.zeros(G.gale_mx_gemm_workspace_size(E, D, T), dtype=torch.uint8, device="cuda")
+        self.ids = torch.zeros(T, K, dtype=torch.int32, device="cuda")
+        self.gates = torch.zeros(T, K, device="cuda")
+        self.ws = torch.zeros(G.gale_moe_workspace_size(layer.desc, T, K), dtype=torch.uint8, device="cuda")
+
+    def run(self):
+        G.gale_rmsnorm(self.x, y=self.y, mx8=self.x8, residual=self.res, weight=self.w1, sum_out=self.h)
+        G.gale_mx_gemm(self.w4, E, D, self.x8, self.logits, self.gemm_ws)
+        G.gale_route_select(self.logits, self.ids, self.gates, bias=self.bias, score=G.GALE_SCORE_SIGMOID,
+                            n_groups=GROUPS[0], keep_groups=GROUPS[1], group_top=GROUPS[2], scale=2.5)
+        G.gale_moe_forward(self.layer.desc, self.y, self.ids, self.gates, self.out, self.ws)
+        G.gale_rmsnorm(self.out, y=self.y2, residual=self.h, weight=self.w2, sum_out=self.h2)
+
+    def outputs(self):
+        return [t.clone() for t in (self.h, self.y, self.logits, self.ids, self.gates, self.out, self.h2, self.y2)]
+
+
+def _f64(t):
+    return t.double().cpu().numpy()
+
+
+def _bf16_close(got, want):
+    # 30 * 2^-24 of the norm and half a unit of bf16
+    assert (np.abs(_f64(got) - want) <= np.abs(want) * (2.0 ** -8 + 2.0 ** -19) + 1e-38).all()
+
+
+@pytest.mark.parametrize("T", [1, 7, 300])
+def test_block_step_by_step(layer, T):
+    b = Block(layer, T)
+    b.run()
+    torch.cuda.synchronize()
+    assert int(b.gemm_ws[:4].view(torch.int32).item()) == 0 and int(b.ws[:4].view(torch.int32).item()) == 0
+    hw, yw = M.rmsnorm(_f64(b.x), _f64(b.res), _f64(b.w1))
+    _bf16_close(b.h, hw)
+    _bf16_close(b.y, yw)
+    codes, k = M.unpack8(b.x8.cpu().numpy(), T, D)
+    xv = M.values(codes[:, :D], k[:, :D // 32], M.GRID8)
+    wv = M.values(*M.quantize(_f64(b.router), M.GRID4), M.GRID4)
+    # products and scales are exact, D / 32 + 34 additions lose a unit in the last place each
+    tol = (D / 32 + 34) * 2.0 ** -23 * (np.abs(xv) @ np.abs(wv).T)
+    assert (np.abs(_f64(b.logits) - xv @ wv.T) <= tol + np.abs(xv @ wv.T) * 2.0 ** -24).all()
+    ids, gates = R.route_select(_f64(b.logits), _f64(b.bias), K, True, *GROUPS, True, 2.5)
+    assert np.array_equal(b.ids.cpu().numpy(), ids)
+    assert (np.abs(_f64(b.gates) - gates) <= 2e-5 * gates).all()
+    sel = np.arange(T) if T < 50 else np.arange(0, T, 13)
+    want = O.moe_layer(layer.dense, _f64(b.y)[sel], ids[sel], _f64(b.gates)[sel])
+    # the layer's own tolerance, and half a unit of its bf16 output
+    assert_tokens(_f64(b.out)[sel], want, tol=2e-3 + 2.0 ** -9, what="experts")
+    hw, yw = M.rmsnorm(_f64(b.out), _f64(b.h), _f64(b.w2))
+    _bf16_close(b.h2, hw)
+    _bf16_close(b.y2, yw)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_block_captured_and_replayed(layer, T):
+    b = Block(layer, T)
+    b.run()
+    torch.cuda.synchronize()
+    want = b.outputs()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        b.run()
+    for t in (b.h, b.y, b.out, b.h2, b.y2, b.logits, b.ids, b.gates):
+        t.zero_()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    for got, w in zip(b.outputs(), want):
+        assert torch.equal(got, w)
+    # other inputs through the same graph
+    b.x.copy_(_normal((T, D), 11).bfloat16())
+    g.replay()
+    torch.cuda.synchronize()
+    got = b.outputs()
+    b.run()
+    torch.cuda.synchronize()
+    for a, w in zip(b.outputs(), got):
+        assert torch.equal(a, w)
+
+
+def test_blocks_on_two_streams(layer):
+    blocks = [Block(layer, T) for T in (8, 33)]
+    want = []
+    for b in blocks:
+        b.run()
+        torch.cuda.synchronize()
+        want.append(b.outputs())
+    streams = [torch.cuda.Stream() for _ in blocks]
+    for _ in range(5):
+        for b, s in zip(blocks, streams):
+            with torch.cuda.stream(s):
+                b.run()
+    torch.cuda.synchronize()
+    for b, w in zip(blocks, want):
+        for x, y in zip(b.outputs(), w):
+            assert torch.equal(x, y)
