@@ -473,14 +473,6 @@ struct GemmPlan {
     int grid, smem;
 };
 
-// Tokens of a tile: all of them up to `most` (the MMA's N in steps of 16), equal
-// tiles of a multiple of 64 beyond (a tile's first scale sits at an even TMEM column).
-int gemm_tile_tokens(int64_t tokens, int most) {
-    if (tokens <= most) return int(align_up(tokens, 16));
-    const int64_t tiles = (tokens + most - 1) / most;
-    return int(align_up((tokens + tiles - 1) / tiles, 64));
-}
-
 // Clusters of `size` CTAs of this kernel that the device holds at once (an SM
 // that is left over in its group of SMs holds none of a larger cluster).
 int gemm_clusters(int size) {
@@ -509,6 +501,14 @@ int gemm_clusters(int size) {
     return found[dev][slot];
 }
 
+// Chooses the tile's tokens, pairs or single CTAs and the split of left-over tiles
+// by an estimate in cycles: a stage of 256 columns takes 4 n + 64 (the tensor
+// pipe), 640 (its issue) or its bytes at 64 a cycle, whichever is longest; a unit
+// some 300 more, 800 from 192 tokens on, 1000 where its accumulators share columns with the last
+// unit's; a join 1500 and 25 a token.  The plan is judged by the mean of its
+// longest CTA and of its average one: many tokens are bound by power, and what
+// idles lets the others run faster.  (1000 tokens x [5000 x 4000]: 192-token
+// pairs 27 us, 256-token pairs 32 us; 4096 x [4096 x 4096]: 58 and 54 us.)
 // False if the device does not answer.
 bool gemm_plan(int64_t rows, int nt, int64_t tokens, GemmPlan& p) {
     GemmArgs& a = p.a;
@@ -516,50 +516,63 @@ bool gemm_plan(int64_t rows, int nt, int64_t tokens, GemmPlan& p) {
     a.tokens = tokens;
     a.nt = nt;
     a.rtiles = int((rows + kMxTile - 1) / kMxTile);
-    p.pair = tokens > kGMaxN;
-    a.n = gemm_tile_tokens(tokens, kGMaxN);
-    a.ntt = int((tokens + a.n - 1) / a.n);
+    const int pieces = (nt + kGK - 1) / kGK;
+    int64_t best = INT64_MAX;
+    int join_bytes = 0;
+    auto consider = [&](bool pair, int n, int split) {
+        const int clusters = gemm_clusters(pair ? 2 : split);
+        if (clusters < 1) return false;
+        const int ntt = int((tokens + n - 1) / n);
+        const int tiles = (pair ? (a.rtiles + 1) / 2 : a.rtiles) * ntt;
+        const int workers = pair ? clusters : clusters * split;
+        const bool joins = !pair && split > 1;
+        const int whole = joins ? tiles / workers : (tiles + workers - 1) / workers;
+        const int left = joins ? tiles - whole * workers : 0;
+        const int joint = (left + clusters - 1) / clusters;
+        if (joins && (joint == 0 || pieces < 2 * split)) return true;
+        const int64_t bytes = joint > 1 ? int64_t(joint) * n * kMxTile * 4 : 0;
+        if (bytes > 64 * 1024) return true;
+        const int64_t load = 2 * (kMx4TileBytes + kMxAtomBytes) + (pair ? n : 2 * n) * int64_t(kMxTile + 4);
+        int64_t step = 4 * n + 64 > 640 ? 4 * n + 64 : 640;
+        if (load / 64 > step) step = load / 64;
+        const int64_t unit = n > 208 ? 1000 : n >= 192 ? 800 : 300;
+        const int64_t tile = pieces * step + unit;
+        const int64_t longest = whole * tile + joint * (((pieces + split - 1) / split) * step + unit) +
+                                (joint ? 1500 + 25 * n : 0);
+        const int64_t cost = longest + tiles * tile / workers + (pair ? 1000 : 0);
+        if (cost < best) {
+            best = cost;
+            p.pair = pair;
+            a.n = n;
+            a.ntt = ntt;
+            a.tiles = tiles;
+            a.split = joins ? split : 1;
+            a.workers = workers;
+            a.whole = whole;
+            a.joint = joint;
+            join_bytes = int(bytes);
+        }
+        return true;
+    };
+    // one tile for all tokens (the MMA's N in steps of 16, of 32 over a pair), or tiles of a multiple of 64 (a tile's first
+    // scale sits at an even TMEM column)
+    const int all = tokens <= kGMaxN ? int(align_up(tokens, 16)) : 0;
+    for (int i = 0; i <= kGMaxN / 64; ++i) {
+        const int n = i == 0 ? all : 64 * i;
+        if (n == 0 || (i > 0 && all > 0 && n >= all)) continue;
+        for (int s = 1; s <= 8; s *= 2)
+            if (!consider(false, n, s)) return false;
+        if (n % 32 == 0 && n >= 64 && !consider(true, n, 1)) return false;
+    }
+    if (p.pair || a.split == 1) {
+        if (a.workers > a.tiles) a.workers = a.tiles;
+    } else if (a.whole == 0 && a.tiles < a.workers / a.split) {
+        a.workers = a.tiles * a.split;      // clusters without a tile are not launched
+    }
+    p.grid = p.pair ? 2 * a.workers : a.workers;
     // tokens t0 .. t0 + n - 1 of a tile that starts at a multiple of n
     a.xatoms = a.ntt == 1 ? (a.n + kMxTile - 1) / kMxTile : a.n % kMxTile == 0 ? a.n / kMxTile : a.n / kMxTile + 2;
     if (a.xatoms > 3) a.xatoms = 3;
-    a.tiles = (p.pair ? (a.rtiles + 1) / 2 : a.rtiles) * a.ntt;
-    int join_bytes = 0;
-    a.split = 1;
-    if (p.pair) {
-        a.workers = gemm_clusters(2);
-        if (a.workers < 1) return false;
-        if (a.workers > a.tiles) a.workers = a.tiles;
-        a.whole = (a.tiles + a.workers - 1) / a.workers;
-        a.joint = 0;
-        p.grid = 2 * a.workers;
-    } else {
-        // The cluster that makes the longest CTA shortest, in column tiles; a join costs about as much as
-        // six of them, and one more for every 32 tokens.
-        int64_t best = INT64_MAX;
-        for (int s = 1; s <= 8; s *= 2) {
-            const int clusters = gemm_clusters(s), workers = clusters * s;
-            if (clusters < 1) return false;
-            const int whole = s == 1 ? (a.tiles + workers - 1) / workers : a.tiles / workers;
-            const int left = s == 1 ? 0 : a.tiles - whole * workers;
-            const int joint = (left + clusters - 1) / clusters;
-            if (s > 1 && (joint == 0 || nt < 2 * kGK * s)) continue;
-            const int64_t bytes = joint > 1 ? int64_t(joint) * a.n * kMxTile * 4 : 0;
-            if (bytes > 64 * 1024) continue;
-            const int64_t cost = int64_t(whole) * nt + int64_t(joint) * ((nt + s - 1) / s) + (joint ? 6 + a.n / 32 : 0);
-            if (cost < best) {
-                best = cost;
-                a.split = s;
-                a.workers = workers;
-                a.whole = whole;
-                a.joint = joint;
-                join_bytes = int(bytes);
-            }
-        }
-        if (a.split == 1 && a.workers > a.tiles) a.workers = a.tiles;
-        // clusters without a tile are not launched
-        if (a.split > 1 && a.whole == 0 && a.tiles < a.workers / a.split) a.workers = a.tiles * a.split;
-        p.grid = a.workers;
-    }
     const int xrows = p.pair ? a.n / 2 : a.n;
     p.resident = !p.pair && a.ntt == 1 && a.xatoms == 1 && nt <= 64;
     const int ncopy = p.resident ? 1 : 1 + a.xatoms;
@@ -606,7 +619,7 @@ extern "C" int gale_mx_gemm(const void* w4, int64_t rows, int64_t cols, const vo
     if (!aligned(ws, 256)) return GALE_ERR_ALIGN;
     const uint8_t* w = static_cast<const uint8_t*>(w4);
     const uint8_t* x = static_cast<const uint8_t*>(x8);
-    if (rows * tokens > (int64_t(1) << 44)) return GALE_ERR_UNSUPPORTED;   // (tiles are counted in 32 bits)
+    if (rows * tokens > (int64_t(1) << 42)) return GALE_ERR_UNSUPPORTED;   // (tiles are counted in 32 bits)
     GemmPlan p{};
     if (!gemm_plan(rows, int(W.cols_padded / kMxTile), tokens, p)) return GALE_ERR_CUDA;
     p.a.wsc = w + W.s_offset;

@@ -366,7 +366,7 @@ int launch_norm_ring(NormArgs& a, cudaStream_t st, bool vec, bool& taken) {
     if (a.stages > 8) a.stages = 8;
     const int64_t most = int64_t(sm_count()) * per_sm;
     // (a row per CTA at most: straight into registers, where that can be, starts sooner)
-    if (chunks > 2048 || a.stages < 2 || (vec && a.tokens <= most)) return GALE_OK;
+    if (chunks > 2048 || a.stages < 2 || (vec && a.tokens <= 4 * most)) return GALE_OK;
     taken = true;
     const unsigned grid = unsigned(a.tokens < most ? a.tokens : most);
     if (a.tokens <= most) a.stages = 1;

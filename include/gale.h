@@ -547,7 +547,7 @@ int gale_mx8_quantize(const void* x, int x_dtype, int64_t ld, int64_t tokens, in
  *        call never clears it and writes GALE_ERR_TIMEOUT there if a bounded
  *        wait inside the kernel ran out (results are then undefined)
  * Any token count (0 is a no-op; GALE_ERR_UNSUPPORTED where rows * tokens
- * passes 2^44).  The sums' order depends on the sizes alone:
+ * passes 2^42).  The sums' order depends on the sizes alone:
  * equal calls give equal bits.
  * Errors: GALE_ERR_ARG, GALE_ERR_ALIGN, GALE_ERR_WORKSPACE,
  * GALE_ERR_UNSUPPORTED, GALE_ERR_CUDA. */

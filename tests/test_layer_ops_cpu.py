@@ -57,6 +57,8 @@ def test_gemm_refusals():
     assert g(P, 64, 128, P, 4, P, G.GALE_F32, 64, P + 16, n, None) == G.GALE_ERR_ALIGN
     assert g(P + 128, 64, 128, P, 4, P, G.GALE_F32, 64, P, n, None) == G.GALE_ERR_ALIGN
     assert g(P, 64, 128, P, 4, P + 2, G.GALE_F32, 64, P, n, None) == G.GALE_ERR_ALIGN
+    big = 1 << 22
+    assert g(P, big, 128, P, big, P, G.GALE_F32, big, P, n, None) == G.GALE_ERR_UNSUPPORTED
 
 
 def test_rmsnorm_refusals():
