@@ -2,8 +2,10 @@
 
 Argument marshalling only: every function forwards torch tensors (device
 memory owned by the caller) as raw pointers to the C ABI declared in
-``include/gale.h``, under the same names.  There is no CPU fallback: if the
-library is missing, loading it raises.
+``include/gale.h``, under the same names, through ctypes; the short calls around
+the experts (router by scores, microscaled formats and product, RMSNorm) through
+a compiled module, which also refuses tensors of the wrong shape, type or
+device.  There is no CPU fallback: if the library is missing, loading it raises.
 """
 from __future__ import annotations
 
@@ -308,38 +310,29 @@ def gale_w4_gemv(packed, rows: int, cols: int, x, y, ws, stream=None):
                               _stream(stream)), "gale_w4_gemv")
 
 
-def _rows2(t, shape, where: str):
-    """Row stride in elements of a [rows, cols] tensor of this shape whose rows are contiguous."""
-    if t.shape != shape:
-        raise GaleError(GALE_ERR_ARG, where + " (a tensor of another shape)")
-    if t.is_contiguous():
-        return shape[1]
-    ld, one = t.stride()
-    if one != 1 and shape[1] > 1:
-        raise GaleError(GALE_ERR_ARG, where + " (rows must be contiguous)")
-    return ld if ld >= shape[1] or shape[0] > 1 else shape[1]
+_fast = None
 
 
-def _mx_room(packed, rows: int, cols: int, mx4: bool, where: str):
-    """Refuse a packed buffer that is smaller than its layout."""
-    rp, cp = (rows + 127) // 128 * 128, (cols + 127) // 128 * 128
-    q = rp * cp // 2 if mx4 else rows * cp
-    if packed.nbytes < (q + 255) // 256 * 256 + rp * cp // 32:
-        raise GaleError(GALE_ERR_ARG, where + " (packed buffer smaller than its layout)")
+def _load_fast():
+    """The compiled argument marshalling of the layer operators (built beside libgale.so)."""
+    global _fast
+    if _fast is None:
+        _load_torch()
+        lib()
+        try:
+            from . import _binding as m
+        except ImportError as e:
+            raise ImportError(f"{HERE}/_binding is missing: run `python -m bit_expert_gemv_b200.build`") from e
+        m.set_error(GaleError)
+        _fast = m
+    return _fast
 
 
 def gale_route_select(logits, ids, gates, bias=None, score: int = GALE_SCORE_SOFTMAX, n_groups: int = 1,
                       keep_groups: int = 1, group_top: int = 1, renorm: bool = True, scale: float = 1.0, stream=None):
     """Top-K experts (K = ids.shape[1]) of every token by score, selection bias and groups, and their gates."""
-    shape, picks = logits.shape, ids.shape
-    B, E = shape
-    if picks != gates.shape or len(picks) != 2 or picks[0] != B or not (ids.is_contiguous() and gates.is_contiguous()):
-        raise GaleError(GALE_ERR_ARG, "gale_route_select (ids and gates are contiguous [B, K])")
-    if bias is not None and (bias.shape != (E,) or not bias.is_contiguous()):
-        raise GaleError(GALE_ERR_ARG, "gale_route_select (bias is [E])")
-    _check(lib().gale_route_select(logits.data_ptr(), _dtype_code(logits), _rows2(logits, shape, "gale_route_select"),
-                                   _ptr(bias), B, E, picks[1], score, n_groups, keep_groups, group_top, 1 if renorm else 0,
-                                   scale, ids.data_ptr(), gates.data_ptr(), _stream(stream)), "gale_route_select")
+    (_fast or _load_fast()).route_select(logits, ids, gates, bias, score, n_groups, keep_groups, group_top, renorm, scale,
+                                       stream)
 
 
 def gale_mx4_layout(rows: int, cols: int) -> gale_mx_layout_t:
@@ -356,26 +349,17 @@ def gale_mx8_layout(tokens: int, cols: int) -> gale_mx_layout_t:
 
 def gale_mx4_quantize(w, packed, stream=None):
     """Quantize a device [rows, cols] matrix to MXFP4 (packed: device bytes of gale_mx4_layout)."""
-    rows, cols = w.shape
-    _mx_room(packed, rows, cols, True, "gale_mx4_quantize")
-    _check(lib().gale_mx4_quantize(_ptr(w), _dtype_code(w), _rows2(w, w.shape, "gale_mx4_quantize"), rows, cols, _ptr(packed),
-                                   _stream(stream)), "gale_mx4_quantize")
+    (_fast or _load_fast()).mx4_quantize(w, packed, stream)
 
 
 def gale_mx4_unpack(packed, out, stream=None):
     """out [rows, cols] = the values a packed MXFP4 matrix stands for."""
-    rows, cols = out.shape
-    _mx_room(packed, rows, cols, True, "gale_mx4_unpack")
-    _check(lib().gale_mx4_unpack(_ptr(packed), rows, cols, _ptr(out), _dtype_code(out),
-                                 _rows2(out, out.shape, "gale_mx4_unpack"), _stream(stream)), "gale_mx4_unpack")
+    (_fast or _load_fast()).mx4_unpack(packed, out, stream)
 
 
 def gale_mx8_quantize(x, packed, stream=None):
     """Quantize device tokens [tokens, cols] to MXFP8 (packed: device bytes of gale_mx8_layout)."""
-    tokens, cols = x.shape
-    _mx_room(packed, tokens, cols, False, "gale_mx8_quantize")
-    _check(lib().gale_mx8_quantize(_ptr(x), _dtype_code(x), _rows2(x, x.shape, "gale_mx8_quantize"), tokens, cols, _ptr(packed),
-                                   _stream(stream)), "gale_mx8_quantize")
+    (_fast or _load_fast()).mx8_quantize(x, packed, stream)
 
 
 def gale_mx_gemm_workspace_size(rows: int, cols: int, tokens: int) -> int:
@@ -384,42 +368,12 @@ def gale_mx_gemm_workspace_size(rows: int, cols: int, tokens: int) -> int:
 
 def gale_mx_gemm(w4, rows: int, cols: int, x8, y, ws, stream=None):
     """y [tokens, rows] = the MXFP8 tokens x8 times the MXFP4 matrix w4 [rows, cols] transposed."""
-    shape = y.shape
-    if len(shape) != 2 or shape[1] != rows:
-        raise GaleError(GALE_ERR_ARG, "gale_mx_gemm (y is [tokens, rows])")
-    _mx_room(w4, rows, cols, True, "gale_mx_gemm")
-    _mx_room(x8, shape[0], cols, False, "gale_mx_gemm")
-    _check(lib().gale_mx_gemm(w4.data_ptr(), rows, cols, x8.data_ptr(), shape[0], y.data_ptr(), _dtype_code(y),
-                              _rows2(y, shape, "gale_mx_gemm"), ws.data_ptr(), ws.nbytes, _stream(stream)),
-           "gale_mx_gemm")
+    (_fast or _load_fast()).mx_gemm(w4, rows, cols, x8, y, ws, stream)
 
 
 def gale_rmsnorm(x, y=None, residual=None, weight=None, sum_out=None, mx8=None, eps: float = 1e-6, stream=None):
     """h = x + residual; y = h / sqrt(mean h^2 + eps) * weight, as y and / or MXFP8 bytes; sum_out = h."""
-    where = "gale_rmsnorm"
-    shape = x.shape
-    tokens, cols = shape
-    dt = x.dtype
-    r = h = out = w = 0
-    ldr = ldh = ldy = wt = yt = 0
-    if residual is not None:
-        r, ldr = residual.data_ptr(), _rows2(residual, shape, where)
-        if residual.dtype != dt:
-            raise GaleError(GALE_ERR_ARG, where + " (residual has x's type)")
-    if sum_out is not None:
-        h, ldh = sum_out.data_ptr(), _rows2(sum_out, shape, where)
-        if sum_out.dtype != dt:
-            raise GaleError(GALE_ERR_ARG, where + " (sum_out has x's type)")
-    if y is not None:
-        out, ldy, yt = y.data_ptr(), _rows2(y, shape, where), _dtype_code(y)
-    if weight is not None:
-        if weight.shape != (cols,) or not weight.is_contiguous():
-            raise GaleError(GALE_ERR_ARG, where + " (weight is [cols])")
-        w, wt = weight.data_ptr(), _dtype_code(weight)
-    if mx8 is not None:
-        _mx_room(mx8, tokens, cols, False, where)
-    _check(lib().gale_rmsnorm(x.data_ptr(), r, _dtype_code(x), _rows2(x, shape, where), ldr, w, wt, eps, tokens, cols, h,
-                              ldh, out, yt, ldy, _ptr(mx8), _stream(stream)), where)
+    (_fast or _load_fast()).rmsnorm(x, y, residual, weight, sum_out, mx8, eps, stream)
 
 
 def make_layer(base, expert_stride: int, n_experts: int, d_model: int, d_ff: int) -> gale_layer:

@@ -291,18 +291,19 @@ __device__ __noinline__ uint32_t exact_groups(const SelectArgs& a, int64_t t, in
 }
 
 // Keys with a bias as fixed point below the token's largest one, `hi`: the
-// fraction bits of key + c in [1, 2), c = 1.9999 - hi, keys further down at 1 +
-// 2^-23, masked ones at 1; over a bit that says the expert exists and its index
-// (inverted).  23 bits (two less for many experts) resolve what fp32 keys can
-// tell, where the leading bits of a float resolved 2^-16 and one token in ten had
-// neighbouring picks in doubt.
+// fraction bits of key * scale + c in [1, 2), c = 1.9999 - hi * scale, keys
+// further down at 1 + 2^-23, masked ones at 1; over a bit that says the expert
+// exists and its index (inverted).  scale is 1, or the power of two that brings
+// the smallest key into the window where a pick lies below it.  23 bits (two less
+// for many experts) resolve what fp32 keys can tell, where the leading bits of a
+// float resolved 2^-16 and one token in ten had neighbouring picks in doubt.
 template <int V>
 struct Fixed {
     static constexpr uint32_t kIndex = 32 * V - 1;
     static constexpr int kLow = V <= 8 ? 9 : V == 16 ? 10 : 11;     // index and existence bits
     static constexpr float kUnit = 1.1920929e-7f * (1 << (kLow - 9));
-    static __device__ __forceinline__ uint32_t pack(float key, float c, int e) {
-        const float f = key == kMinusInf ? 1.0f : fmaxf(key + c, 1.0000001f);
+    static __device__ __forceinline__ uint32_t pack(float key, float scale, float c, int e) {
+        const float f = key == kMinusInf ? 1.0f : fmaxf(fmaf(key, scale, c), 1.0000001f);
         return ((__float_as_uint(f) << 9) & ~((1u << kLow) - 1u)) | (1u << (kLow - 1)) | (kIndex - e);
     }
     static __device__ __forceinline__ int expert(uint32_t m) { return int(kIndex - (m & kIndex)); }
@@ -314,8 +315,8 @@ struct Fixed {
 // their 64-bit keys.  False if an expert that is not among them could still
 // belong to the picks.
 template <int V>
-__device__ __noinline__ bool refine(const SelectArgs& a, int64_t t, int lane, int n, float margin, float c, float lmax,
-                                    uint32_t m, int& pick) {
+__device__ __noinline__ bool refine(const SelectArgs& a, int64_t t, int lane, int n, float margin, float scale, float c,
+                                    float lmax, uint32_t m, int& pick) {
     using F = Fixed<V>;
     const bool live = lane < n && m != 0u;
     const uint32_t last = __shfl_sync(0xffffffffu, m, n - 1);
@@ -345,8 +346,8 @@ __device__ __noinline__ bool refine(const SelectArgs& a, int64_t t, int lane, in
         if (r == a.K - 1) kth = o;
     }
     // a key that is not among the n is at most the last one's
-    const float most = 1.0f + float(F::fraction(last) + 1) * F::kUnit - c;
-    return last == 0u || F::fraction(last) == 0 || kth - most > margin;
+    const float most = 1.0f + float(F::fraction(last) + 1) * F::kUnit - c;      // (in the window's scale)
+    return last == 0u || F::fraction(last) == 0 || fmaf(kth, scale, -most) > margin * scale;
 }
 
 // The sum over lanes 0 .. K - 1 (zeros from K on), valid in those lanes.
@@ -615,23 +616,37 @@ __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_ke
             for (int j = 0; j < V; ++j) hi = stays(lane + 32 * j) ? fmaxf(hi, s[j]) : hi;
             hi = warp_max_t(hi);
             sure = sure && hi < INFINITY;
-            if (sure) {
-                const float c = hi == kMinusInf ? 0.f : 1.9999f - hi;
-                // what two keys' difference may be off by: the scores, their roundings with the bias and with c
-                const float margin = 2.0f * es + 2.4e-7f * (fmaxf(fabsf(hi), 0.f) + 2.0f);
+            // what two keys' difference may be off by: the scores, their roundings with the bias and in the window
+            const float margin = 2.0f * es + 2.4e-7f * (fabsf(hi) + 2.0f);
+            float scale = 1.0f;
+#pragma unroll 1
+            while (sure) {
+                const float c = hi == kMinusInf ? 0.f : fmaf(-hi, scale, 1.9999f);
 #pragma unroll
-                for (int j = 0; j < V; ++j) pk[j] = stays(lane + 32 * j) ? F::pack(s[j], c, lane + 32 * j) : 0u;
+                for (int j = 0; j < V; ++j) pk[j] = stays(lane + 32 * j) ? F::pack(s[j], scale, c, lane + 32 * j) : 0u;
                 // one more than is picked: the last pick's lead counts too
                 const uint32_t m = take_packed<V>(pk, a.K + 1, lane);
                 const uint32_t next = __shfl_down_sync(0xffffffffu, m, 1);
                 id = F::expert(m);
+                // (margin in the window's scale, and the window's own rounding)
+                const float off = fmaf(margin, scale, 2.4e-7f);
                 const bool clear = lane >= a.K || next == 0u || F::fraction(next) == 0 ||
-                                   float(F::fraction(m) - F::fraction(next) - 1) * F::kUnit > margin;
-                if (!__all_sync(0xffffffffu, clear)) {
-                    const int n = a.K + 3;
-                    const uint32_t mn = take_packed<V>(pk, n, lane);
-                    sure = refine<V>(a, t, lane, n, margin, c, lmax, mn, id);
+                                   float(F::fraction(m) - F::fraction(next) - 1) * F::kUnit > off;
+                if (__all_sync(0xffffffffu, clear)) break;
+                if (scale == 1.0f && __any_sync(0xffffffffu, lane <= a.K && m != 0u && F::fraction(m) == 1)) {
+                    float lo = INFINITY;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) lo = stays(lane + 32 * j) && s[j] > kMinusInf ? fminf(lo, s[j]) : lo;
+                    lo = -warp_max_t(-lo);
+                    if (hi - lo < 1e30f) {
+                        scale = exp2f(-ceilf(log2f((hi - lo) * 1.01f)));
+                        if (scale < 1.0f) continue;
+                    }
                 }
+                const int n = a.K + 3;
+                const uint32_t mn = take_packed<V>(pk, n, lane);
+                sure = refine<V>(a, t, lane, n, margin + 2.4e-7f / scale, scale, c, lmax, mn, id);
+                break;
             }
         } else {
 #pragma unroll

@@ -99,6 +99,19 @@ def test_select_masks_and_extremes(sigmoid, biased, groups):
     _run(l, 6, _bias(64, 2) if biased else None, sigmoid, groups)
 
 
+@pytest.mark.parametrize("spread", [0.5, 2.0, 30.0, 1e4, 1e20])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_select_wide_biases(sigmoid, spread):
+    # keys far below the largest: picks outside a window of one, down to keys that the bias swallows
+    l = _logits(60, 256, 12)
+    b = _bias(256, 13, spread)
+    _run(l, 8, b, sigmoid)
+    _run(l, 8, b, sigmoid, (8, 3, 2))
+    b[::2] = -1e9                                # a mask by a large finite value
+    _run(l, 16, b, sigmoid)
+    _run(l, 16, b, sigmoid, (8, 1, 2))
+
+
 def test_select_bias_extremes():
     b = _bias(64, 4)
     b[3], b[9], b[20] = float("inf"), -float("inf"), float("nan")
