@@ -207,3 +207,50 @@ def test_gemm_other_stream_graph_and_two_workspaces():
     torch.cuda.synchronize()
     for y, ws in outs:
         assert torch.equal(y, want) and int(ws[:4].view(torch.int32).item()) == 0
+
+
+def test_gemm_behind_copies_and_other_kernels():
+    """The product's set-up may overlap the kernel before it: behind memory sets,
+    copies, library kernels and its own kind, eagerly and captured, it reads what
+    they wrote."""
+    rows, cols, tokens = 1024, 512, 40
+    ws_ = [_matrix(rows, cols, s) for s in (1, 2)]
+    xs = [_matrix(tokens, cols, s, "bf16") for s in (3, 4)]
+    packs = [_pack4(w) for w in ws_]
+    want = [[_gemm(p, rows, cols, _pack8(x), tokens).clone() for x in xs] for p in packs]
+    w4, x8 = torch.zeros_like(packs[0]), torch.zeros(G.gale_mx8_layout(tokens, cols).total, dtype=torch.uint8, device="cuda")
+    x = torch.zeros_like(xs[0])
+    y = [torch.zeros(tokens, rows, device="cuda") for _ in range(6)]
+    ws = torch.zeros(G.gale_mx_gemm_workspace_size(rows, cols, tokens), dtype=torch.uint8, device="cuda")
+
+    def run():
+        x.copy_(xs[0])
+        G.gale_mx8_quantize(x, x8)
+        w4.copy_(packs[0])                                     # a copy right before the product
+        G.gale_mx_gemm(w4, rows, cols, x8, y[0], ws)
+        G.gale_mx_gemm(packs[1], rows, cols, x8, y[1], ws)     # behind its own kind
+        x.copy_(xs[1])
+        G.gale_mx8_quantize(x, x8)                             # overwrites what the last product read
+        G.gale_mx_gemm(w4, rows, cols, x8, y[2], ws)
+        G.gale_mx4_quantize(ws_[1], w4)                        # overwrites its weights
+        G.gale_mx_gemm(w4, rows, cols, x8, y[3], ws)
+        y[4].zero_()                                           # a memory set right before
+        G.gale_mx_gemm(w4, rows, cols, x8, y[4], ws)
+        torch.add(y[4], 1.0, out=y[5])                         # a library kernel behind
+
+    def check():
+        torch.cuda.synchronize()
+        for got, w in zip(y, (want[0][0], want[1][0], want[0][1], want[1][1], want[1][1], want[1][1] + 1.0)):
+            assert torch.equal(got, w)
+
+    for _ in range(3):
+        run()
+    check()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        run()
+    for t in y:
+        t.zero_()
+    for _ in range(4):
+        g.replay()
+    check()
