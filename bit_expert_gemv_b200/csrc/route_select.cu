@@ -244,6 +244,10 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, int64_t t, int lan
     return mine;
 }
 
+// The float of order bits (the inverse of the function below).
+__device__ __forceinline__ float order_value(uint32_t o) {
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
 // Unsigned order of a float: larger value, larger integer (-0 as +0); 0 is below every value's.
 __device__ __forceinline__ uint32_t order_bits(float f) {
     const uint32_t u = __float_as_uint(f + 0.0f);
@@ -357,11 +361,12 @@ __device__ __forceinline__ T picks_sum(int K, T v) {
     return v;
 }
 
-// Gates of the picks (lane k holds pick k), written with the ids.  `lmax` and
+// Gates of the picks (lane k holds pick k and its logit `l`), written with the ids.  `lmax` and
 // `sum`: the softmax's maximum and denominator, read where they are needed.
-__device__ __forceinline__ void write_picks(const SelectArgs& a, int64_t t, int lane, int id, float lmax, float sum) {
+__device__ __forceinline__ void write_picks(const SelectArgs& a, int64_t t, int lane, int id, float l, float lmax,
+                                            float sum) {
     const bool on = lane < a.K;
-    const float l = on ? logit_at(a, t, id) : kMinusInf;
+    if (!on) l = kMinusInf;
     float g, z;
     if (a.sigmoid) {
         g = __fdividef(1.0f, 1.0f + __expf(-l));      // 0 past the last pick
@@ -467,14 +472,14 @@ template <int V>
 __device__ __forceinline__ uint32_t take_packed(const uint32_t (&pk)[V], int n, int lane) {
     uint32_t h1, h2, h3, mine = 0u;
     lane_top3<V, false>(pk, 0u, h1, h2, h3);
-    for (int k = 0; k < n; ++k) {
+    auto round = [&](int k, bool third) {
         const uint32_t m = __reduce_max_sync(0xffffffffu, h1);
         mine = lane == k ? m : mine;
         const bool own = h1 == m;
         h1 = own ? h2 : h1;
         h2 = own ? h3 : h2;
         h3 = own ? 0u : h3;
-        if (V > 3 && __any_sync(0xffffffffu, own && h1 == 0u)) {
+        if (V > 3 && third && __any_sync(0xffffffffu, own && h1 == 0u)) {
             uint32_t g1, g2, g3;
             lane_top3<V, true>(pk, m, g1, g2, g3);
             if (own) {
@@ -483,7 +488,12 @@ __device__ __forceinline__ uint32_t take_packed(const uint32_t (&pk)[V], int n, 
                 h3 = g3;
             }
         }
-    }
+    };
+    // (a lane has given its third key in the third round at the earliest)
+    round(0, false);
+    if (n > 1) round(1, false);
+#pragma unroll 2
+    for (int k = 2; k < n; ++k) round(k, true);
     return mine;
 }
 
@@ -529,13 +539,19 @@ __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_ke
         const bool whole = a.dtype != GALE_F32;
         const uint32_t m = take_packed<V>(pk, whole ? a.K : a.K + 1, lane);
         id = int(kIndex - (m & kIndex));
-        if (!whole) {
-            const uint32_t next = __shfl_down_sync(0xffffffffu, m, 1);
-            if (__any_sync(0xffffffffu, lane < a.K && next != 0u && ((m ^ next) & ~kIndex) == 0u)) {
+        if (whole) {
+            // the pick's logit from its key: a negative one's order bits end in ones, and so do those of
+            // the largest finite fp32, for which an infinity stands
+            const uint32_t o = m & ~kIndex, ones = m | kIndex;
+            const bool low = !(o & 0x80000000u) || ones == 0xFF7FFFFFu;
+            write_picks(a, t, lane, id, order_value(low ? ones : o), lmax, sum);
+            return;
+        }
+        const uint32_t next = __shfl_down_sync(0xffffffffu, m, 1);
+        if (__any_sync(0xffffffffu, lane < a.K && next != 0u && ((m ^ next) & ~kIndex) == 0u)) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) pk[j] = lane + 32 * j < a.E ? order_bits(l[j]) : 0u;
-                id = take_largest<V>(pk, a.K, lane);
-            }
+            for (int j = 0; j < V; ++j) pk[j] = lane + 32 * j < a.E ? order_bits(l[j]) : 0u;
+            id = take_largest<V>(pk, a.K, lane);
         }
     } else {
         // fp32 scores are needed of every expert with a bias, else of the groups' best;
@@ -666,7 +682,7 @@ __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_ke
         }
         if (!sure) id = select_exact<V>(a, t, lane);
     }
-    write_picks(a, t, lane, id, lmax, sum);
+    write_picks(a, t, lane, id, lane < a.K ? logit_at(a, t, id) : kMinusInf, lmax, sum);
 }
 
 }  // namespace

@@ -76,9 +76,10 @@ def test_select_groups(E, groups, K, sigmoid, biased, dtype):
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("biased", [False, True])
 @pytest.mark.parametrize("groups", [(1, 1, 1), (8, 3, 2)])
-def test_select_masks_and_extremes(sigmoid, biased, groups):
-    l = _logits(16, 64, 1)
-    inf, big = float("inf"), float(np.finfo(np.float32).max)
+@pytest.mark.parametrize("dtype,renorm", [("f32", True), ("f32", False), ("bf16", False), ("bf16", True), ("f16", False)])
+def test_select_masks_and_extremes(sigmoid, biased, groups, dtype, renorm):
+    l = _logits(16, 64, 1, dtype)
+    inf, big = float("inf"), float(torch.finfo(DT[dtype]).max)
     l[0] = -inf                                  # nothing is left
     l[1] = float("nan")
     l[2, 3:] = -inf                              # fewer experts than picks
@@ -96,7 +97,7 @@ def test_select_masks_and_extremes(sigmoid, biased, groups):
     l[14] = 1e-20 * l[14]
     l[15] = -0.0
     l[15, 30] = 0.0
-    _run(l, 6, _bias(64, 2) if biased else None, sigmoid, groups)
+    _run(l, 6, _bias(64, 2) if biased else None, sigmoid, groups, renorm=renorm)
 
 
 @pytest.mark.parametrize("spread", [0.5, 2.0, 30.0, 1e4, 1e20])
