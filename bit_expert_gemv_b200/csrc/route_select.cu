@@ -83,15 +83,18 @@ __device__ __forceinline__ T with_bias(T s, float b, bool masked) {
     return masked || !(k == k) ? T(-INFINITY) : k;
 }
 
-template <typename T>
-__device__ __forceinline__ T warp_max_t(T v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const T u = __shfl_xor_sync(0xffffffffu, v, o);
-        v = u > v ? u : v;
-    }
-    return v;
+// The float of order bits (the inverse of the function below).
+__device__ __forceinline__ float order_value(uint32_t o) {
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
+// Unsigned order of a float: larger value, larger integer (-0 as +0); 0 is below every value's.
+__device__ __forceinline__ uint32_t order_bits(float f) {
+    const uint32_t u = __float_as_uint(f + 0.0f);
+    return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+}
+// The warp's largest value, by one integer reduction (no NaN; -0 may come back as +0).
+__device__ __forceinline__ float warp_max_f(float v) { return order_value(__reduce_max_sync(0xffffffffu, order_bits(v))); }
+
 template <typename T>
 __device__ __forceinline__ T warp_sum_t(T v) {
 #pragma unroll
@@ -143,6 +146,7 @@ __device__ __forceinline__ double group_scores(const SelectArgs& a, const double
 template <typename T>
 __device__ __forceinline__ uint32_t kept_groups(const SelectArgs& a, T score, int lane) {
     int rank = 0;
+#pragma unroll 4
     for (int g = 0; g < a.groups; ++g) {
         const T o = __shfl_sync(0xffffffffu, score, g);
         rank += o > score || (o == score && g < lane);
@@ -194,7 +198,7 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, int64_t t, int lan
     float lmax = kMinusInf;
 #pragma unroll
     for (int j = 0; j < V; ++j) lmax = fmaxf(lmax, l[j]);
-    lmax = fmaxf(warp_max_t(lmax), -kFltMax);
+    lmax = fmaxf(warp_max_f(lmax), -kFltMax);
     double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -242,16 +246,6 @@ __device__ __noinline__ int select_exact(const SelectArgs& a, int64_t t, int lan
         if (lane == k) mine = bi;
     }
     return mine;
-}
-
-// The float of order bits (the inverse of the function below).
-__device__ __forceinline__ float order_value(uint32_t o) {
-    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
-}
-// Unsigned order of a float: larger value, larger integer (-0 as +0); 0 is below every value's.
-__device__ __forceinline__ uint32_t order_bits(float f) {
-    const uint32_t u = __float_as_uint(f + 0.0f);
-    return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
 }
 
 // Whether a >= b is certain to be the order of the 64-bit values when either
@@ -384,7 +378,7 @@ __device__ __forceinline__ void write_picks(const SelectArgs& a, int64_t t, int 
     } else if (a.renorm) {
         // relative to the largest pick: the softmax's denominator cancels
         float m = l;
-        if (a.bias) m = warp_max_t(l);
+        if (a.bias) m = warp_max_f(l);
         else m = __shfl_sync(0xffffffffu, l, 0);
         g = __expf(l - fmaxf(m, -kFltMax));
         z = picks_sum(a.K, g);
@@ -513,7 +507,13 @@ __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_ke
     const int lane = threadIdx.x & 31;
     const int64_t t = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
     if (t >= a.B) return;
-    float l[V];
+    float l[V], bias[SCORED ? V : 1];
+    if constexpr (SCORED) {      // (asked for before the logits are waited for)
+        if (a.bias) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) bias[j] = lane + 32 * j < a.E ? __ldg(a.bias + lane + 32 * j) : 0.f;
+        }
+    }
     load_logits<V>(a, t, lane, l);
     float lmax = kMinusInf, sum = 0.f;
     uint32_t pk[V];
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_ke
     if (!a.sigmoid && (SCORED || !a.renorm)) {
 #pragma unroll
         for (int j = 0; j < V; ++j) lmax = fmaxf(lmax, l[j]);
-        lmax = fmaxf(warp_max_t(lmax), -kFltMax);
+        lmax = fmaxf(warp_max_f(lmax), -kFltMax);
     }
     if constexpr (!SCORED) {
         if (!a.sigmoid && !a.renorm) {
@@ -584,10 +584,7 @@ __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_ke
                 for (int j = 0; j < V; ++j) s[j] = __expf(l[j] - lmax) * inv;
             }
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int e = lane + 32 * j;
-                s[j] = with_bias(s[j], e < a.E ? __ldg(a.bias + e) : 0.f, l[j] == kMinusInf);
-            }
+            for (int j = 0; j < V; ++j) s[j] = with_bias(s[j], bias[j], l[j] == kMinusInf);
         }
         uint32_t kept = 0xFFFFFFFFu;
         bool sure = true;
@@ -602,12 +599,12 @@ __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_ke
             const float k1 = a.bias || m1 == kMinusInf ? m1 : score32(a, m1, lmax, inv);
             const float k2 = a.bias || m2 == kMinusInf ? m2 : score32(a, m2, lmax, inv);
             const float f1 = fabsf(k1), f2 = fabsf(k2);
-            const float big = warp_max_t(fmaxf(f1 < INFINITY ? f1 : 0.f, f2 < INFINITY ? f2 : 0.f));
+            const float big = warp_max_f(fmaxf(f1 < INFINITY ? f1 : 0.f, f2 < INFINITY ? f2 : 0.f));
             const float score = group_sum(k1, k2);
             kept = kept_groups(a, score, lane);
             const bool in = (kept >> lane) & 1u;
-            const float worst = -warp_max_t(in ? -score : kMinusInf);
-            const float best = warp_max_t(lane < a.groups && !in ? score : kMinusInf);
+            const float worst = -warp_max_f(in ? -score : kMinusInf);
+            const float best = warp_max_f(lane < a.groups && !in ? score : kMinusInf);
             sure = certain(worst, best, 2.0f * es + 4.8e-7f * big);
             if (!sure && !a.bias) {
                 // the best two of a group are certain (by logit): their scores in 64 bits
@@ -630,7 +627,7 @@ __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_ke
             float hi = kMinusInf;
 #pragma unroll
             for (int j = 0; j < V; ++j) hi = stays(lane + 32 * j) ? fmaxf(hi, s[j]) : hi;
-            hi = warp_max_t(hi);
+            hi = warp_max_f(hi);
             sure = sure && hi < INFINITY;
             // what two keys' difference may be off by: the scores, their roundings with the bias and in the window
             const float margin = 2.0f * es + 2.4e-7f * (fabsf(hi) + 2.0f);
@@ -653,7 +650,7 @@ __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_ke
                     float lo = INFINITY;
 #pragma unroll
                     for (int j = 0; j < V; ++j) lo = stays(lane + 32 * j) && s[j] > kMinusInf ? fminf(lo, s[j]) : lo;
-                    lo = -warp_max_t(-lo);
+                    lo = -warp_max_f(-lo);
                     if (hi - lo < 1e30f) {
                         scale = exp2f(-ceilf(log2f((hi - lo) * 1.01f)));
                         if (scale < 1.0f) continue;
