@@ -296,10 +296,10 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
                 }
             }
         }
-        // the last copies land before the CTA may end (bounded)
-        if (!ok)
-            for (int i = max(0, issued - a.stages); i < issued; ++i)
-                mbar_wait_warp(full0 + i % a.stages * 8, (i / a.stages) & 1);
+        // before the CTA may end (bounded): the last stages' MMAs have reported, or after a failure the last
+        // copies have landed
+        for (int i = max(0, issued - a.stages); i < issued; ++i)
+            ok = mbar_wait_warp((ok ? empty0 : full0) + i % a.stages * 8, (i / a.stages) & 1) && ok;
     } else if (warp == 1 && (!PAIR || rank == 0)) {
         const bool lead = elect_one();
         const uint32_t idesc = umma_idesc_mx(PAIR ? 2 * kMxTile : kMxTile, a.n);
@@ -458,8 +458,10 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
     }
     tc_fence_before();
     __syncthreads();
-    // nobody reads a peer's partial sums, reads its operands or arrives on its barriers after this
-    if (PAIR || a.split > 1) cluster_sync();
+    // nobody reads a peer's partial sums, reads its operands or arrives on its barriers after this (reads have
+    // returned when their values were used; arrivals need the release)
+    if (PAIR) cluster_sync();
+    else if (a.split > 1) cluster_sync_relaxed();
     if (warp == 3) {
         tc_fence_after();
         if (PAIR) tmem_dealloc_pair(tmem, a.cols);

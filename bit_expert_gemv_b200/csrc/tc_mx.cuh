@@ -198,6 +198,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same without ordering memory: only to keep a CTA alive until its peers have
+// read its shared memory (the values they read have been used by then).
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 // Four floats at the same shared-memory address in CTA `rank` of the cluster.
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr, uint32_t rank) {
     uint32_t remote;
