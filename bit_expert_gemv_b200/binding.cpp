@@ -134,6 +134,15 @@ PyObject* guarded(const char* name, Py_ssize_t have, Py_ssize_t want, F f) {
     Py_RETURN_NONE;
 }
 
+// The library's call, with other Python threads running meanwhile (a full launch queue blocks).
+template <typename F>
+int unlocked(F f) {
+    PyThreadState* state = PyEval_SaveThread();
+    const int rc = f();
+    PyEval_RestoreThread(state);
+    return rc;
+}
+
 PyObject* route_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded("gale_route_select", n, 11, [&] {
         Call c;
@@ -148,10 +157,15 @@ PyObject* route_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Call::flat(gates, at::kFloat, B * K);
         if (bias) Call::flat(bias, at::kFloat, E);
         const int dt = logits.dtype();
-        return gale_route_select(logits.ptr(), dt, ld, static_cast<const float*>(bias.ptr()), int(B), int(E), int(K),
-                                 int(whole(a[4])), int(whole(a[5])), int(whole(a[6])), int(whole(a[7])),
-                                 PyObject_IsTrue(a[8]) == 1, real(a[9]), static_cast<int32_t*>(ids.ptr()),
-                                 static_cast<float*>(gates.ptr()), c.stream(a[10]));
+        const int score = int(whole(a[4])), groups = int(whole(a[5])), keep = int(whole(a[6])), top = int(whole(a[7]));
+        const int renorm = PyObject_IsTrue(a[8]) == 1;
+        const float scale = real(a[9]);
+        void* s = c.stream(a[10]);
+        return unlocked([&] {
+            return gale_route_select(logits.ptr(), dt, ld, static_cast<const float*>(bias.ptr()), int(B), int(E), int(K),
+                                     score, groups, keep, top, renorm, scale, static_cast<int32_t*>(ids.ptr()),
+                                     static_cast<float*>(gates.ptr()), s);
+        });
     });
 }
 
@@ -164,8 +178,10 @@ PyObject* quantize(const char* name, bool mx4, PyObject* const* a, Py_ssize_t n)
         Call::room(packed, mx4, r, k);
         const int dt = x.dtype();
         void* s = c.stream(a[2]);
-        return mx4 ? gale_mx4_quantize(x.ptr(), dt, ld, r, k, packed.ptr(), s)
-                   : gale_mx8_quantize(x.ptr(), dt, ld, r, k, packed.ptr(), s);
+        return unlocked([&] {
+            return mx4 ? gale_mx4_quantize(x.ptr(), dt, ld, r, k, packed.ptr(), s)
+                       : gale_mx8_quantize(x.ptr(), dt, ld, r, k, packed.ptr(), s);
+        });
     });
 }
 PyObject* mx4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) { return quantize("gale_mx4_quantize", true, a, n); }
@@ -178,7 +194,9 @@ PyObject* mx4_unpack(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (out.t->dim() != 2) throw Refused{"a [rows, cols] tensor"};
         const int64_t r = out.size(0), k = out.size(1), ld = Call::rows(out, r, k);
         Call::room(packed, true, r, k);
-        return gale_mx4_unpack(packed.ptr(), r, k, out.ptr(), out.dtype(), ld, c.stream(a[2]));
+        const int dt = out.dtype();
+        void* s = c.stream(a[2]);
+        return unlocked([&] { return gale_mx4_unpack(packed.ptr(), r, k, out.ptr(), dt, ld, s); });
     });
 }
 
@@ -194,8 +212,10 @@ PyObject* mx_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Call::room(x8, false, tokens, cols);
         const int dt = y.dtype();
         const int64_t room = Call::bytes(ws);
-        return gale_mx_gemm(w4.ptr(), rows, cols, x8.ptr(), tokens, y.ptr(), dt, ldy, ws.ptr(), size_t(room),
-                            c.stream(a[6]));
+        void* s = c.stream(a[6]);
+        return unlocked([&] {
+            return gale_mx_gemm(w4.ptr(), rows, cols, x8.ptr(), tokens, y.ptr(), dt, ldy, ws.ptr(), size_t(room), s);
+        });
     });
 }
 
@@ -210,9 +230,14 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if ((r && r.dtype() != dt) || (h && h.dtype() != dt)) throw Refused{"residual and sum_out have x's type"};
         if (w) Call::flat(w, w.t->scalar_type(), k);
         if (q) Call::room(q, false, t, k);
-        return gale_rmsnorm(x.ptr(), r.ptr(), dt, ldx, r ? Call::rows(r, t, k) : 0, w.ptr(), w ? w.dtype() : 0,
-                            real(a[6]), t, k, h.ptr(), h ? Call::rows(h, t, k) : 0, y.ptr(), y ? y.dtype() : 0,
-                            y ? Call::rows(y, t, k) : 0, q.ptr(), c.stream(a[7]));
+        const int64_t ldr = r ? Call::rows(r, t, k) : 0, ldh = h ? Call::rows(h, t, k) : 0, ldy = y ? Call::rows(y, t, k) : 0;
+        const int wt = w ? w.dtype() : 0, yt = y ? y.dtype() : 0;
+        const float eps = real(a[6]);
+        void* s = c.stream(a[7]);
+        return unlocked([&] {
+            return gale_rmsnorm(x.ptr(), r.ptr(), dt, ldx, ldr, w.ptr(), wt, eps, t, k, h.ptr(), ldh, y.ptr(), yt, ldy,
+                                q.ptr(), s);
+        });
     });
 }
 

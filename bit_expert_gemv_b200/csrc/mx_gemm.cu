@@ -504,14 +504,14 @@ int gemm_clusters(int size) {
 }
 
 // Chooses the tile's tokens, pairs or single CTAs and the split of left-over tiles
-// by an estimate in cycles: a stage of 256 columns takes 4 n + 64 (the tensor
+// by an estimate in cycles.  A stage of 256 columns takes 4 n + 64 (the tensor
 // pipe), 640 (its issue) or its bytes at 64 a cycle, whichever is longest; a unit
-// some 300 more, 800 from 192 tokens on, 1000 where its accumulators share columns with the last
-// unit's; a join 1500 and 25 a token.  The plan is judged by the mean of its
-// longest CTA and of its average one: many tokens are bound by power, and what
-// idles lets the others run faster.  (1000 tokens x [5000 x 4000]: 192-token
-// pairs 27 us, 256-token pairs 32 us; 4096 x [4096 x 4096]: 58 and 54 us.)
-// False if the device does not answer.
+// some 300 more, 800 from 192 tokens on, 1000 where its accumulators share columns
+// with the last unit's; a join 1500 and 25 a token.  What counts is the sum of the
+// longest CTA's time and the average one's: many tokens are bound by power, and
+// what idles lets the others run faster.  (1000 tokens x [5000 x 4000]: 192-token
+// pairs 27 us, 256-token pairs 32 us; 4096 x [4096 x 4096]: 58 and 54 us.)  False
+// if the device does not answer.
 bool gemm_plan(int64_t rows, int nt, int64_t tokens, GemmPlan& p) {
     GemmArgs& a = p.a;
     a.rows = rows;
@@ -556,8 +556,8 @@ bool gemm_plan(int64_t rows, int nt, int64_t tokens, GemmPlan& p) {
         }
         return true;
     };
-    // one tile for all tokens (the MMA's N in steps of 16, of 32 over a pair), or tiles of a multiple of 64 (a tile's first
-    // scale sits at an even TMEM column)
+    // one tile for all tokens (the MMA's N in steps of 16, of 32 over a pair), or tiles of a multiple of 64 (a
+    // tile's first scale sits at an even TMEM column)
     const int all = tokens <= kGMaxN ? int(align_up(tokens, 16)) : 0;
     for (int i = 0; i <= kGMaxN / 64; ++i) {
         const int n = i == 0 ? all : 64 * i;

@@ -301,7 +301,8 @@ struct Fixed {
     static constexpr int kLow = V <= 8 ? 9 : V == 16 ? 10 : 11;     // index and existence bits
     static constexpr float kUnit = 1.1920929e-7f * (1 << (kLow - 9));
     static __device__ __forceinline__ uint32_t pack(float key, float scale, float c, int e) {
-        const float f = key == kMinusInf ? 1.0f : fmaxf(fmaf(key, scale, c), 1.0000001f);
+        // (c's rounding may carry the largest keys of a large bias to 2: they tie below it, in doubt)
+        const float f = key == kMinusInf ? 1.0f : fminf(fmaxf(fmaf(key, scale, c), 1.0000001f), 1.9999999f);
         return ((__float_as_uint(f) << 9) & ~((1u << kLow) - 1u)) | (1u << (kLow - 1)) | (kIndex - e);
     }
     static __device__ __forceinline__ int expert(uint32_t m) { return int(kIndex - (m & kIndex)); }
@@ -411,8 +412,9 @@ __device__ __forceinline__ void lane_top2(const uint32_t (&key)[V], uint32_t tak
 }
 
 // Picks 0 .. n - 1 by descending key, the lower expert first on equal keys: lane
-// k returns pick k's expert.  Every round takes the largest of the lanes' heads; a lane that gives its head moves its
-// second up, and looks through its keys again only when it gives a third.
+// k returns pick k's expert.  Every round takes the largest of the lanes' heads; a
+// lane that gives its head moves its second up, and looks through its keys again
+// only when it gives a third.
 template <int V>
 __device__ __forceinline__ int take_largest(const uint32_t (&key)[V], int n, int lane) {
     uint32_t taken = 0u, h1, h2;
@@ -605,7 +607,9 @@ __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_ke
             const bool in = (kept >> lane) & 1u;
             const float worst = -warp_max_f(in ? -score : kMinusInf);
             const float best = warp_max_f(lane < a.groups && !in ? score : kMinusInf);
-            sure = certain(worst, best, 2.0f * es + 4.8e-7f * big);
+            // (a sum of two finite keys that leaves fp32's range tells nothing)
+            sure = certain(worst, best, 2.0f * es + 4.8e-7f * big) &&
+                   !__any_sync(0xffffffffu, score > kFltMax && k1 <= kFltMax);
             if (!sure && !a.bias) {
                 // the best two of a group are certain (by logit): their scores in 64 bits
                 const double all = a.sigmoid ? 1.0 : softmax_sum64<V>(l, lmax);

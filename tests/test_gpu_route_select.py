@@ -113,6 +113,18 @@ def test_select_wide_biases(sigmoid, spread):
     _run(l, 16, b, sigmoid, (8, 1, 2))
 
 
+@pytest.mark.parametrize("offset", [-3e3, 1e3, 3e3, 1e4, 1e5, 1e7, 1e15, 2.5e38])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_select_large_biases(sigmoid, offset):
+    # a bias that all experts share up to a little: the window's own offset rounds, and sums of two leave fp32
+    l = _logits(60, 256, 14)
+    b = (_bias(256, 15, 0.3).double() + offset).float()
+    _run(l, 8, b, sigmoid)
+    _run(l, 8, b, sigmoid, (8, 3, 2))
+    b = (offset * (1 + 0.2 * _bias(256, 16, 1.0).double().clamp(-1, 1))).float()
+    _run(l, 8, b, sigmoid, (8, 3, 2))
+
+
 def test_select_bias_extremes():
     b = _bias(64, 4)
     b[3], b[9], b[20] = float("inf"), -float("inf"), float("nan")

@@ -120,3 +120,14 @@ def test_binding_refuses_wrong_shapes():
         G.gale_mx4_quantize(x, torch.zeros(64, dtype=torch.uint8), stream=0)
     with pytest.raises(G.GaleError):
         G.gale_route_select(x, torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, 4), stream=0)
+    with pytest.raises(G.GaleError):                              # 64-bit ids
+        G.gale_route_select(x, torch.zeros(4, 4, dtype=torch.int64), torch.zeros(4, 4), stream=0)
+    with pytest.raises(G.GaleError):                              # a bias of another size
+        G.gale_route_select(x, torch.zeros(4, 4, dtype=torch.int32), torch.zeros(4, 4), bias=torch.zeros(63), stream=0)
+    with pytest.raises(G.GaleError):                              # integers are no weights
+        G.gale_mx8_quantize(torch.zeros(4, 64, dtype=torch.int32), torch.zeros(4096, dtype=torch.uint8), stream=0)
+    with pytest.raises(G.GaleError):                              # a missing tensor
+        G.gale_mx_gemm(None, 64, 64, x, x, x, stream=0)
+    with pytest.raises(G.GaleError) as e:                         # all right but for the device
+        G.gale_rmsnorm(x, y=x, stream=0)
+    assert e.value.code == G.GALE_ERR_ARG and "device" in str(e.value)
