@@ -165,6 +165,7 @@ def _ptr(t):
 
 _torch = None
 _codes = None       # torch dtype -> dtype code
+_cuda_ready = False
 
 
 def _load_torch():
@@ -176,9 +177,13 @@ def _load_torch():
 
 
 def _stream(stream):
+    global _cuda_ready
     if stream is None:
         # the current stream's handle, without building a Stream object (3 us) on every call
-        c = (_torch or _load_torch())._C
+        if not _cuda_ready:
+            (_torch or _load_torch()).cuda.init()
+            _cuda_ready = True
+        c = _torch._C
         return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     if isinstance(stream, int):
         return stream
