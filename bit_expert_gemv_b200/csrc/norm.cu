@@ -179,34 +179,23 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) rmsnorm_kernel(const __grid_
     }
 }
 
-// h of the columns c .. c + 7 straight from the row, 0 outside it.
-template <int DT>
-__device__ __forceinline__ void ring_edge(const NormArgs& a, int64_t row, int c, float (&h)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int e = c + i;
-        float v = 0.f;
-        if (e >= 0 && e < a.cols) {
-            v = load_as_f32(a.x, DT, row * a.ldx + e);
-            if (a.r) v += load_as_f32(a.r, DT, row * a.ldr + e);
-        }
-        h[i] = v;
-    }
-}
-
 // A CTA per row, rows blockIdx.x, + gridDim.x, ...: thread 0 keeps the next
 // `stages` rows' bulk copies in flight.  Rows whose length is no multiple of
 // eight start at any element; every tensor's row starts at the same element
-// modulo 8 (`phase`), so chunks of eight that are aligned in one are in all: a
+// modulo 8 (its phase), so chunks of eight that are aligned in one are in all: a
 // copy takes the aligned bytes around its row (inside the tensor for every row
-// but the last, whose last chunk is read directly), and the first and the last
-// chunk hold columns of the neighbouring rows, which are masked.
+// but the last, whose last columns are fetched one by one), and the first and
+// the last chunk hold columns of the neighbouring rows, which are masked.
 //
-// The weights are in registers before a row's stores are issued (for all rows at
-// once where the rows' phase is always 0): a load behind the stores waited
-// thousands of cycles in the saturated memory pipeline.
+// The weights stay in registers, loaded once: a load behind the stores waited
+// thousands of cycles in the saturated memory pipeline.  So a CTA's rows have
+// one phase, the grid being a multiple of eight CTAs (10007 x 5001 in fp32 74
+// us, with weights loaded for every row 94; registers bounded so that the CTAs
+// the launch counts on fit).  A row held in registers between its two passes
+// beats one read twice from its stage by fewer warps (4096 x 4096 in 16 bits 24
+// against 34 us: half the unpacking).
 template <int DT, int CH, bool PHASED>
-__global__ void __launch_bounds__(512) rmsnorm_ring_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(CH == 1 ? 256 : 512, CH == 1 ? 6 : CH == 2 ? 2 : 1) rmsnorm_ring_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ float part[2][16];
     __shared__ uint64_t full[8];
@@ -218,23 +207,8 @@ __global__ void __launch_bounds__(512) rmsnorm_ring_kernel(const __grid_constant
         fence_mbar_init();
     }
     __syncthreads();
-    auto phase_of = [&](int64_t row) { return PHASED ? int((row * a.ldx) & 7) : 0; };
-    float w[CH][8];
-    auto load_w = [&](int ph) {
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            const int c = (j * threads + t) * 8 - ph;
-            if (a.w) {
-                norm_weights(a, c, c < 0 ? -c : 0, a.cols - c, w[j]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[j][i] = 1.0f;
-            }
-        }
-    };
-    if (!PHASED) load_w(0);
+    const int ph = PHASED ? int((blockIdx.x * a.ldx) & 7) : 0;
     auto issue = [&](int64_t row, int s) {
-        const int ph = phase_of(row);
         int bytes = ((ph + a.cols) * ES + 15) & ~15;
         if (row + 1 == a.tokens) bytes = (ph + a.cols) * ES & ~15;
         uint8_t* st = ring + s * a.stage_bytes;
@@ -249,20 +223,37 @@ __global__ void __launch_bounds__(512) rmsnorm_ring_kernel(const __grid_constant
             const int64_t row = blockIdx.x + int64_t(s) * gridDim.x;
             if (row < a.tokens) issue(row, s);
         }
+    float w[CH][8];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        const int c = (j * threads + t) * 8 - ph;
+        if (a.w) {
+            norm_weights(a, c, c < 0 ? -c : 0, a.cols - c, w[j]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[j][i] = 1.0f;
+        }
+    }
     int s = 0, turn = 0;
     uint32_t parity = 0;
     for (int64_t row = blockIdx.x; row < a.tokens; row += gridDim.x) {
         const bool here = mbar_wait_cycles(&full[s], parity);
-        const int ph = phase_of(row);
-        const int have = row + 1 == a.tokens ? (ph + a.cols) * ES / 16 * (16 / ES) - ph : INT32_MAX;   // columns copied
-        const uint8_t* st = ring + s * a.stage_bytes;
+        uint8_t* st = ring + s * a.stage_bytes;
+        if (row + 1 == a.tokens && (ph + a.cols) * ES % 16) {      // what the copy left out
+            for (int e = ((ph + a.cols) * ES & ~15) / ES + t; e < ph + a.cols; e += threads) {
+                using T = std::conditional_t<DT == GALE_F32, uint32_t, uint16_t>;
+                reinterpret_cast<T*>(st)[e] = static_cast<const T*>(a.x)[row * a.ldx - ph + e];
+                if (a.r) reinterpret_cast<T*>(st + a.r_off)[e] = static_cast<const T*>(a.r)[row * a.ldr - ph + e];
+            }
+            __syncthreads();
+        }
         float h[CH][8];
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             const int k = j * threads + t;
             const int c = k * 8 - ph;
-            if (c < a.cols && c + 8 <= have) {
+            if (c < a.cols) {
                 Raw8<DT> x;
                 load_raw8<DT, true>(st, k * 8, 8, x);
                 raw8_f32<DT>(x, h[j]);
@@ -278,13 +269,13 @@ __global__ void __launch_bounds__(512) rmsnorm_ring_kernel(const __grid_constant
                     for (int i = 0; i < 8; ++i) h[j][i] = c + i >= 0 && c + i < a.cols ? h[j][i] : 0.f;
                 }
             } else {
-                ring_edge<DT>(a, row, c, h[j]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[j][i] = 0.f;
             }
             if (!here) h[j][0] = __uint_as_float(0x7FC00000u);      // the bounded wait ran out: the row is NaN
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss = fmaf(h[j][i], h[j][i], ss);
         }
-        if (PHASED) load_w(ph);
         ss = warp_sum(ss);
         // (two buffers: a fast warp's next row does not reach into a slow one's read)
         if (lane == 0) part[turn][t >> 5] = ss;
@@ -368,7 +359,8 @@ int launch_norm_ring(NormArgs& a, cudaStream_t st, bool vec, bool& taken) {
     // (a row per CTA at most: straight into registers, where that can be, starts sooner)
     if (chunks > 2048 || a.stages < 2 || (vec && a.tokens <= 4 * most)) return GALE_OK;
     taken = true;
-    const unsigned grid = unsigned(a.tokens < most ? a.tokens : most);
+    // a multiple of eight CTAs takes rows of one phase each
+    const unsigned grid = unsigned(a.tokens <= most ? a.tokens : a.ldx % 8 ? most / 8 * 8 : most);
     if (a.tokens <= most) a.stages = 1;
     const int smem = a.stages * a.stage_bytes;
     auto go = [&](auto kern) {
