@@ -6,11 +6,10 @@
 // fp32, before its rounding to the residual's type.  y leaves in 16 or 32 bits
 // and / or as MXFP8 (e4m3 codes, one power-of-two scale per 32 columns).
 //
-// Three kernels: up to 256 columns a warp per row; beyond, a CTA per row, whose
-// rows arrive by bulk copies in a ring of shared-memory stages (registers alone
-// do not hold enough rows in flight: 31 us against the ring's time at 4096 x
-// 4096 in 16 bits); rows too wide for the ring, or not aligned for it, straight
-// into registers.
+// A row goes straight into registers: of a warp up to 512 columns, of a CTA
+// beyond.  Many wide rows in 16 bits cost more instructions per byte than that
+// hides: theirs arrive by bulk copies in a ring of shared-memory stages (4096 x
+// 4096 with residual 24 us, 31 us without the ring).
 #include "mx.cuh"
 #include "ptx.cuh"
 #include "tma.cuh"
@@ -65,20 +64,27 @@ __device__ __forceinline__ void mx8_store_scalar(const NormArgs& a, int64_t row,
     if ((threadIdx.x & 31) == 0) a.s[mx_scale_at(row, c / kMxBlock, a.nt)] = uint8_t(b);
 }
 
-// Eight columns' worth of a row as loaded.  VEC: from column c; otherwise the
-// single elements c + i * threads.
-template <int DT, bool VEC>
+// How a row is read and written: eight neighbouring columns of a thread 16 bytes
+// at a time, the row starting on a chunk of eight (kVec) or anywhere (kPhased:
+// chunks that are aligned in memory, the first and the last of which the row may
+// fill in part); or single elements `threads` apart (kSingle).
+enum { kSingle, kVec, kPhased };
+
+// Eight columns' worth of a row as loaded, from column c (kSingle: c + i *
+// threads); zero outside the row.
+template <int DT, int HOW>
 __device__ __forceinline__ void norm_load(const void* p, int64_t at, int cols, int c, int threads, Raw8<DT>& v) {
-    if constexpr (VEC) {
+    if (HOW == kVec || (HOW == kPhased && c >= 0 && c + 8 <= cols)) {
         load_raw8<DT, true>(p, at + c, cols - c, v);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int e = c + i * threads;
+            const int e = HOW == kPhased ? c + i : c + i * threads;
+            const bool in = e < cols && (HOW == kSingle || e >= 0);
             if constexpr (DT == GALE_F32) {
-                v.u[i] = e < cols ? static_cast<const uint32_t*>(p)[at + e] : 0u;
+                v.u[i] = in ? static_cast<const uint32_t*>(p)[at + e] : 0u;
             } else {
-                const uint32_t h = e < cols ? uint32_t(static_cast<const uint16_t*>(p)[at + e]) : 0u;
+                const uint32_t h = in ? uint32_t(static_cast<const uint16_t*>(p)[at + e]) : 0u;
                 v.u[i / 2] = i % 2 ? v.u[i / 2] | h << 16 : h;
             }
         }
@@ -105,11 +111,21 @@ __device__ __forceinline__ void norm_weights(const NormArgs& a, int c, int lo, i
     }
 }
 
+// The columns c .. c + 7 of a row, `n` of them up to the row's end (a phased row's first chunk begins before it).
+__device__ __forceinline__ void norm_store(void* p, int dtype, int64_t at, int c, int n, bool whole, const float (&v)[8]) {
+    if (whole) {
+        if (n > 0) store8(p, dtype, at, n, true, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i >= 0 && i < n) store_rn(p, dtype, at + i, v[i]);
+    }
+}
+
 // A row per group of `threads` threads (a warp, or the CTA), CH * 8 columns per
-// thread.  VEC: thread t holds columns (j * threads + t) * 8 + i, read and
-// written 16 bytes at a time; otherwise (j * 8 + i) * threads + t, single
-// elements, for rows that are not 16-byte aligned.
-template <int DT, bool VEC, int CH, bool WARP>
+// thread: (j * threads + t) * 8 + i less the row's phase, or, kSingle, (j * 8 +
+// i) * threads + t.
+template <int DT, int HOW, int CH, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : 512) rmsnorm_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float part[16];
     if (a.q) pdl_launch_dependents();      // a product behind this kernel may set itself up meanwhile
@@ -120,11 +136,13 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) rmsnorm_kernel(const __grid_
     if (row >= a.tokens) return;      // whole warps (a CTA always has its row)
     float h[CH][8];
     float ss = 0.f;
+    constexpr bool VEC = HOW != kSingle;
+    const int ph = HOW == kPhased ? int((row * a.ldx) & 7) : 0;
     const int stride = VEC ? threads * 8 : threads;      // between a thread's columns j and j + 1 (VEC) / elements
     Raw8<DT> x[CH];
 #pragma unroll
     for (int j = 0; j < CH; ++j)
-        norm_load<DT, VEC>(a.x, row * a.ldx, a.cols, VEC ? j * stride + t * 8 : j * 8 * stride + t, threads, x[j]);
+        norm_load<DT, HOW>(a.x, row * a.ldx, a.cols, VEC ? j * stride + t * 8 - ph : j * 8 * stride + t, threads, x[j]);
 #pragma unroll
     for (int j = 0; j < CH; ++j) raw8_f32<DT>(x[j], h[j]);
     if (a.r) {
@@ -132,7 +150,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) rmsnorm_kernel(const __grid_
         for (int j = 0; j < CH; ++j) {
             Raw8<DT> raw;
             float r[8];
-            norm_load<DT, VEC>(a.r, row * a.ldr, a.cols, VEC ? j * stride + t * 8 : j * 8 * stride + t, threads, raw);
+            norm_load<DT, HOW>(a.r, row * a.ldr, a.cols, VEC ? j * stride + t * 8 - ph : j * 8 * stride + t, threads, raw);
             raw8_f32<DT>(raw, r);
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[j][i] += r[i];
@@ -152,18 +170,19 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) rmsnorm_kernel(const __grid_
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
         if constexpr (VEC) {
-            const int c = j * stride + t * 8;
+            const int c = j * stride + t * 8 - ph;
             const int n = a.cols - c;
+            const bool whole = HOW == kVec || (c >= 0 && n >= 8);
             float w[8];
-            if (a.w) norm_weights(a, c, 0, n, w);
-            if (a.h && n > 0) store8(a.h, DT, row * a.ldh + c, n, true, h[j]);
+            if (a.w) norm_weights(a, c, c < 0 ? -c : 0, n, w);
+            if (a.h) norm_store(a.h, DT, row * a.ldh + c, c, n, whole, h[j]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float y = h[j][i] * inv;
                 h[j][i] = i < n ? (a.w ? y * w[i] : y) : 0.f;
             }
-            if (a.y && n > 0) store8(a.y, a.yt, row * a.ldy + c, n, true, h[j]);
-            if (a.q) mx8_store_vec(a, row, c, h[j], c < a.span);
+            if (a.y) norm_store(a.y, a.yt, row * a.ldy + c, c, n, whole, h[j]);
+            if (HOW == kVec && a.q) mx8_store_vec(a, row, c, h[j], c < a.span);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -298,7 +317,8 @@ __global__ void __launch_bounds__(CH == 1 ? 256 : 512, CH == 1 ? 6 : CH == 2 ? 2
                 if (a.h) store8(a.h, DT, row * a.ldh + c, 8, true, h[j]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * inv * w[j][i];
-                if (a.y) store8(a.y, a.yt, row * a.ldy + c, 8, true, h[j]);
+                if (DT != GALE_F32 && a.y && a.yt == DT) store8(a.y, DT, row * a.ldy + c, 8, true, h[j]);
+                else if (a.y) store8(a.y, a.yt, row * a.ldy + c, 8, true, h[j]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -316,48 +336,47 @@ __global__ void __launch_bounds__(CH == 1 ? 256 : 512, CH == 1 ? 6 : CH == 2 ? 2
 constexpr int kNormMaxCols = 32768;
 
 // Rows straight into registers.
-template <int DT, bool VEC>
+template <int DT, int HOW>
 void launch_norm(const NormArgs& a, cudaStream_t st) {
-    const int chunks = (a.span + 7) / 8;             // eight-column chunks of a row
-    if (chunks <= 128) {                             // up to 1024 columns: a warp per row, eight rows per CTA
+    const int chunks = (a.span + 7) / 8 + (HOW == kPhased ? 1 : 0);             // eight-column chunks of a row
+    if (chunks <= 64) {                              // up to 512 columns: a warp per row, eight rows per CTA
         const unsigned grid = unsigned((a.tokens + 7) / 8);
-        if (chunks <= 32) rmsnorm_kernel<DT, VEC, 1, true><<<grid, 256, 0, st>>>(a);
-        else if (chunks <= 64) rmsnorm_kernel<DT, VEC, 2, true><<<grid, 256, 0, st>>>(a);
-        else rmsnorm_kernel<DT, VEC, 4, true><<<grid, 256, 0, st>>>(a);
-    } else {                                         // a CTA per row
+        if (chunks <= 32) rmsnorm_kernel<DT, HOW, 1, true><<<grid, 256, 0, st>>>(a);
+        else rmsnorm_kernel<DT, HOW, 2, true><<<grid, 256, 0, st>>>(a);
+    } else {                                         // a CTA per row (148 rows of 704 columns: 2.4 us, a warp each 4.7)
         const unsigned grid = unsigned(a.tokens);
         const int ch = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8;
         const int threads = ((chunks + ch - 1) / ch + 31) / 32 * 32;
-        if (ch == 1) rmsnorm_kernel<DT, VEC, 1, false><<<grid, threads, 0, st>>>(a);
-        else if (ch == 2) rmsnorm_kernel<DT, VEC, 2, false><<<grid, threads, 0, st>>>(a);
-        else if (ch == 4) rmsnorm_kernel<DT, VEC, 4, false><<<grid, threads, 0, st>>>(a);
-        else rmsnorm_kernel<DT, VEC, 8, false><<<grid, threads, 0, st>>>(a);
+        if (ch == 1) rmsnorm_kernel<DT, HOW, 1, false><<<grid, threads, 0, st>>>(a);
+        else if (ch == 2) rmsnorm_kernel<DT, HOW, 2, false><<<grid, threads, 0, st>>>(a);
+        else if (ch == 4) rmsnorm_kernel<DT, HOW, 4, false><<<grid, threads, 0, st>>>(a);
+        else rmsnorm_kernel<DT, HOW, 8, false><<<grid, threads, 0, st>>>(a);
     }
 }
 
 // Rows through the ring; false if it does not take them.
 template <int DT>
-int launch_norm_ring(NormArgs& a, cudaStream_t st, bool vec, bool& taken) {
-    const int es = DT == GALE_F32 ? 4 : 2;
+int launch_norm_ring(NormArgs& a, cudaStream_t st, bool& taken) {
+    const int es = 2;
     taken = false;
     const int chunks = (a.span + 7) / 8 + (a.ldx % 8 ? 1 : 0);
     const int row_bytes = chunks * 8 * es;
     a.r_off = row_bytes;
     a.stage_bytes = a.r ? 2 * row_bytes : row_bytes;
-    // 32 columns per thread: what a row costs every thread (barrier, sums, addresses) weighs least
+    // columns per thread: what a row costs every thread (barrier, sums, addresses) weighs least with many, the latency
+    // of a row least with few (4096 x 4096 in 16 bits: 16 of them 17.4 us, 32 19.5; 4000 x 6000: 24.5
+    // and 30.5)
     const int ch = chunks <= 256 ? 1 : chunks <= 1024 ? 2 : 4;
     const int threads = ((chunks + ch - 1) / ch + 31) / 32 * 32;
-    // CTAs of an SM by its registers; at least two stages each
-    constexpr int kRoom = 220 * 1024;
+    // CTAs of an SM by its registers (20,000 x 400 in 16 bits: 24 of them 15 us, 8 of them 19); two stages each
+    auto room = [](int ctas) { return 228 * 1024 / ctas - 1536; };      // shared memory of each, static and reserved off
     int per_sm = (ch == 4 ? 512 : ch == 2 ? 1024 : 1536) / threads;
-    if (per_sm > 8) per_sm = 8;
     if (per_sm < 1) per_sm = 1;
-    while (per_sm > 1 && kRoom / per_sm < 2 * a.stage_bytes) --per_sm;
-    a.stages = kRoom / per_sm / a.stage_bytes;
+    while (per_sm > 1 && room(per_sm) < 2 * a.stage_bytes) --per_sm;
+    a.stages = room(per_sm) / a.stage_bytes;
     if (a.stages > 8) a.stages = 8;
     const int64_t most = int64_t(sm_count()) * per_sm;
-    // (a row per CTA at most: straight into registers, where that can be, starts sooner)
-    if (chunks > 2048 || a.stages < 2 || (vec && a.tokens <= 4 * most)) return GALE_OK;
+    if (chunks > 2048 || a.stages < 2) return GALE_OK;
     taken = true;
     // a multiple of eight CTAs takes rows of one phase each
     const unsigned grid = unsigned(a.tokens <= most ? a.tokens : a.ldx % 8 ? most / 8 * 8 : most);
@@ -426,22 +445,33 @@ extern "C" int gale_rmsnorm(const void* x, const void* residual, int dtype, int6
     cudaStream_t st = as_stream(stream);
     const bool vec = rows_vec(x, dtype, ldx) && (!residual || rows_vec(residual, dtype, ldr)) &&
                      (!sum_out || rows_vec(sum_out, dtype, ldsum)) && (!y || rows_vec(y, y_dtype, ldy));
-    // bases on 16 bytes and row strides that agree modulo 8 elements: the ring (with MXFP8, whose blocks start
-    // with the row, only if rows start on chunks of eight)
+    // bases on 16 bytes and row strides that agree modulo 8 elements: rows in aligned chunks (with MXFP8, whose blocks
+    // start with the row, only if rows start on chunks of eight)
     auto agrees = [&](const void* p, int64_t ld) { return !p || (aligned(p, 16) && (ld - ldx) % 8 == 0); };
-    if (a.span > 256 && agrees(x, ldx) && agrees(residual, ldr) && agrees(sum_out, ldsum) && agrees(y, ldy) &&
-        (!mx8 || ldx % 8 == 0)) {
+    const bool phased = a.span > 256 && agrees(x, ldx) && agrees(residual, ldr) && agrees(sum_out, ldsum) &&
+                        agrees(y, ldy) && (!mx8 || ldx % 8 == 0);
+    // The ring pays where a row costs many instructions per byte and there are rows enough: in 16 bits, from 1024
+    // columns and 4.5 M elements on (with residual: 4736 x 4096 21 us, straight into registers 32; 20,000 x 704 20 each;
+    // 592 x 5000 5.9 and 5.2).  In fp32 registers are ahead everywhere (10,007 x 5000: 67 us, ring 78).
+    if (phased && dtype != GALE_F32 && cols >= 1024 && tokens * cols >= 4500000) {
         bool taken = false;
-        const int rc = dtype == GALE_F32    ? launch_norm_ring<GALE_F32>(a, st, vec, taken)
-                       : dtype == GALE_BF16 ? launch_norm_ring<GALE_BF16>(a, st, vec, taken)
-                                            : launch_norm_ring<GALE_F16>(a, st, vec, taken);
+        const int rc = dtype == GALE_BF16 ? launch_norm_ring<GALE_BF16>(a, st, taken)
+                                          : launch_norm_ring<GALE_F16>(a, st, taken);
         if (rc != GALE_OK) return rc;
         if (taken) {
             GALE_LAUNCH_CHECK();
             return GALE_OK;
         }
     }
-    by_dtype_vec(dtype, vec, [&](auto dt, auto v) { launch_norm<decltype(dt)::value, decltype(v)::value>(a, st); });
+    auto direct = [&](auto how) {
+        constexpr int HOW = decltype(how)::value;
+        if (dtype == GALE_F32) launch_norm<GALE_F32, HOW>(a, st);
+        else if (dtype == GALE_BF16) launch_norm<GALE_BF16, HOW>(a, st);
+        else launch_norm<GALE_F16, HOW>(a, st);
+    };
+    if (vec) direct(std::integral_constant<int, kVec>());
+    else if (phased) direct(std::integral_constant<int, kPhased>());
+    else direct(std::integral_constant<int, kSingle>());
     GALE_LAUNCH_CHECK();
     return GALE_OK;
 }

@@ -125,6 +125,22 @@ def test_norm_zero_nan_and_inf_rows(cols):
     _close(y[rows], M.rmsnorm(x[rows].double().cpu().numpy())[1], "f32")
 
 
+@pytest.mark.parametrize("tokens,cols", [(520, 9000), (520, 9001), (330, 16384), (330, 16387), (2, 9003), (1, 300), (9, 511)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("res", [False, True])
+def test_norm_wide_rows_and_few(tokens, cols, dtype, out, res):
+    # rows of the ring's widest form and past it, and single rows that start at any element
+    x = _rand((tokens, cols), cols, dtype)
+    r = _rand((tokens, cols), cols + 1, dtype) if res else None
+    w = 1 + 0.1 * _rand((cols,), 3, dtype).float()
+    y = torch.full((tokens * cols + 8,), 7.0, dtype=DT[out], device="cuda")
+    yv = y[:tokens * cols].view(tokens, cols)
+    G.gale_rmsnorm(x, y=yv, residual=r, weight=w)
+    _, yw = M.rmsnorm(x.double().cpu().numpy(), r.double().cpu().numpy() if res else None, w.double().cpu().numpy())
+    _close(yv, yw, out)
+    assert (y[tokens * cols:] == 7).all()
+
+
 @pytest.mark.parametrize("cols", [40, 257, 700, 1001, 2000, 4093, 5001])
 @pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f32", "f32"), ("f16", "f16")])
 def test_norm_many_rows_of_every_width(cols, dtype, out):
