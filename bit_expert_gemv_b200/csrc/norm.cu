@@ -54,6 +54,24 @@ __device__ __forceinline__ void mx8_store_vec(const NormArgs& a, int64_t row, in
     if ((threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(a.s + mx_scale_at(row, c / kMxBlock, a.nt)) = word;
 }
 
+// MXFP8 of four columns per thread: eight neighbouring threads hold a block.
+__device__ __forceinline__ void mx8_store_vec(const NormArgs& a, int64_t row, int c, const float (&v)[4], bool live) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
+    const uint32_t b = mx8_scale_byte(m);
+    uint32_t word = b << (8 * ((threadIdx.x >> 3) & 3));
+    word |= __shfl_xor_sync(0xffffffffu, word, 8);
+    word |= __shfl_xor_sync(0xffffffffu, word, 16);
+    if (!live) return;
+    *reinterpret_cast<uint32_t*>(a.q + row * a.nt * kMxTile + c) =
+        b != 255u ? mx8_codes(v[0], v[1], v[2], v[3], mx_inverse(b)) : 0u;
+    if ((threadIdx.x & 31) == 0) *reinterpret_cast<uint32_t*>(a.s + mx_scale_at(row, c / kMxBlock, a.nt)) = word;
+}
+
 __device__ __forceinline__ void mx8_store_scalar(const NormArgs& a, int64_t row, int c, float v, bool live) {
     // a warp's 32 consecutive columns are one block
     const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu);
@@ -64,102 +82,167 @@ __device__ __forceinline__ void mx8_store_scalar(const NormArgs& a, int64_t row,
     if ((threadIdx.x & 31) == 0) a.s[mx_scale_at(row, c / kMxBlock, a.nt)] = uint8_t(b);
 }
 
-// How a row is read and written: eight neighbouring columns of a thread 16 bytes
-// at a time, the row starting on a chunk of eight (kVec) or anywhere (kPhased:
-// chunks that are aligned in memory, the first and the last of which the row may
-// fill in part); or single elements `threads` apart (kSingle).
-enum { kSingle, kVec, kPhased };
-
-// Eight columns' worth of a row as loaded, from column c (kSingle: c + i *
-// threads); zero outside the row.
-template <int DT, int HOW>
-__device__ __forceinline__ void norm_load(const void* p, int64_t at, int cols, int c, int threads, Raw8<DT>& v) {
-    if (HOW == kVec || (HOW == kPhased && c >= 0 && c + 8 <= cols)) {
-        load_raw8<DT, true>(p, at + c, cols - c, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int e = HOW == kPhased ? c + i : c + i * threads;
-            const bool in = e < cols && (HOW == kSingle || e >= 0);
-            if constexpr (DT == GALE_F32) {
-                v.u[i] = in ? static_cast<const uint32_t*>(p)[at + e] : 0u;
-            } else {
-                const uint32_t h = in ? uint32_t(static_cast<const uint16_t*>(p)[at + e]) : 0u;
-                v.u[i / 2] = i % 2 ? v.u[i / 2] | h << 16 : h;
-            }
+// What a thread takes at a time: 16 bytes of a row, E columns, so that a warp's accesses are contiguous.
+template <int DT>
+struct Unit {
+    static constexpr int E = DT == GALE_F32 ? 4 : 8;
+    uint4 v;
+    __device__ __forceinline__ void f32(float (&h)[E]) const {
+        if constexpr (DT == GALE_F32) {
+            h[0] = __uint_as_float(v.x); h[1] = __uint_as_float(v.y);
+            h[2] = __uint_as_float(v.z); h[3] = __uint_as_float(v.w);
+        } else {
+            const Raw8<DT> r{{v.x, v.y, v.z, v.w}};
+            raw8_f32<DT>(r, h);
         }
     }
-}
+};
 
-// The weights of columns c .. c + 7, `lo` to `n` - 1 of which exist.
-__device__ __forceinline__ void norm_weights(const NormArgs& a, int c, int lo, int n, float (&w)[8]) {
-    if (a.wt == GALE_F32 && a.vw && lo == 0 && n >= 8 && (c & 3) == 0) {
-        Raw8<GALE_F32> u;
-        load_raw8<GALE_F32, true>(a.w, c, 8, u);
-        raw8_f32<GALE_F32>(u, w);
-    } else if (a.wt == GALE_F32 && a.vw && c >= 4 && c + 12 <= a.cols) {
-        // eight of the twelve from the 16-byte boundary before
-        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(a.w) + (c & ~3));
-        const float4 f0 = q[0], f1 = q[1], f2 = q[2];
-        const float f[12] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w, f2.x, f2.y, f2.z, f2.w};
-        const int sh = c & 3;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = sh == 0 ? f[i] : sh == 1 ? f[i + 1] : sh == 2 ? f[i + 2] : f[i + 3];
+template <int E>
+__device__ __forceinline__ void store_unit(void* p, int dtype, int64_t at, const float (&v)[E]) {
+    if constexpr (E == 8) {
+        store8(p, dtype, at, 8, true, v);
+    } else if (dtype == GALE_F32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = i >= lo && i < n ? load_as_f32(a.w, a.wt, c + i) : 0.f;
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) =
+            make_uint2(pack16(dtype, v[0], v[1]), pack16(dtype, v[2], v[3]));
     }
 }
 
-// The columns c .. c + 7 of a row, `n` of them up to the row's end (a phased row's first chunk begins before it).
-__device__ __forceinline__ void norm_store(void* p, int dtype, int64_t at, int c, int n, bool whole, const float (&v)[8]) {
-    if (whole) {
-        if (n > 0) store8(p, dtype, at, n, true, v);
+// How a row is read and written: units of neighbouring columns, the row starting
+// on a unit (kVec) or anywhere (kPhased: units that are aligned in memory, the
+// first and the last of which the row may fill in part); or single elements
+// `threads` apart (kSingle).
+enum { kSingle, kVec, kPhased };
+
+// A unit of a row as loaded, from column c (kSingle: c + i * threads); zero outside the row.
+template <int DT, int HOW>
+__device__ __forceinline__ void norm_load(const void* p, int64_t at, int cols, int c, int threads, Unit<DT>& v) {
+    constexpr int E = Unit<DT>::E;
+    if (HOW != kSingle && (HOW == kVec || c >= 0) && c + E <= cols) {
+        v.v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + (at + c) * (16 / E));
+    } else {
+        uint32_t u[4] = {};
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int e = HOW == kSingle ? c + i * threads : c + i;
+            if (e >= cols || (HOW == kPhased && e < 0)) continue;
+            if constexpr (DT == GALE_F32) u[i] = static_cast<const uint32_t*>(p)[at + e];
+            else u[i / 2] |= uint32_t(static_cast<const uint16_t*>(p)[at + e]) << (16 * (i % 2));
+        }
+        v.v = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+}
+
+// The weights of columns c .. c + E - 1, `lo` to `n` - 1 of which exist.
+template <int E>
+__device__ __forceinline__ void norm_weights(const NormArgs& a, int c, int lo, int n, float (&w)[E]) {
+    const bool whole = lo == 0 && n >= E && a.vw;
+    if (a.wt == GALE_F32 && whole && (c & 3) == 0) {
+#pragma unroll
+        for (int q = 0; q < E / 4; ++q) {
+            const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(a.w) + c + 4 * q);
+            w[4 * q] = f.x; w[4 * q + 1] = f.y; w[4 * q + 2] = f.z; w[4 * q + 3] = f.w;
+        }
+    } else if (a.wt == GALE_F32 && whole && c >= 4 && n >= E + 4) {
+        // E of the E + 4 from the 16-byte boundary before
+        float f[E + 4];
+        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(a.w) + (c & ~3));
+#pragma unroll
+        for (int i = 0; i < E / 4 + 1; ++i) {
+            const float4 v = q[i];
+            f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
+        }
+        if (c & 2) {
+#pragma unroll
+            for (int i = 0; i < E + 1; ++i) f[i] = f[i + 2];
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) w[i] = c & 1 ? f[i + 1] : f[i];
+    } else if (a.wt != GALE_F32 && whole && (c & (E - 1)) == 0) {
+        uint32_t u[E / 2];
+        const uint16_t* q = static_cast<const uint16_t*>(a.w) + c;
+        if constexpr (E == 8) {
+            const uint4 v = *reinterpret_cast<const uint4*>(q);
+            u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(q);
+            u[0] = v.x; u[1] = v.y;
+        }
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            const float2 f = a.wt == GALE_BF16 ? make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u))
+                                               : __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+            w[2 * i] = f.x;
+            w[2 * i + 1] = f.y;
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < E; ++i) w[i] = i >= lo && i < n ? load_as_f32(a.w, a.wt, c + i) : 0.f;
+    }
+}
+
+// The columns c .. c + E - 1 of a row, `n` of them up to the row's end (a phased row's first unit begins before it).
+template <int E>
+__device__ __forceinline__ void norm_store(void* p, int dtype, int64_t at, int c, int n, const float (&v)[E]) {
+    if (c >= 0 && n >= E) {
+        store_unit<E>(p, dtype, at, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i)
             if (c + i >= 0 && i < n) store_rn(p, dtype, at + i, v[i]);
     }
 }
 
 // A row per group of `threads` threads (a warp, or the CTA), CH * 8 columns per
-// thread: (j * threads + t) * 8 + i less the row's phase, or, kSingle, (j * 8 +
-// i) * threads + t.
+// thread: (j * threads + t) * E + i less the row's phase, or, kSingle, (j * E +
+// i) * threads + t.  Units of 16 bytes in fp32 too, so that a warp's access is
+// one run of 512 bytes; all of a row's loads, then all of its residual's, are
+// asked for before the first is used (10,007 x 5000 fp32: 67 -> 65 us, with
+// residual 95 -> 88).  Registers are bounded for as many CTAs as keep HBM busy:
+// 50 instead of 48 of them for two chunks cost a fourth CTA at 5000 columns, 74
+// us.
 template <int DT, int HOW, int CH, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 512) rmsnorm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __maxnreg__(CH == 1 ? 40 : CH == 2 ? 48 : CH == 4 ? 64 : 128) rmsnorm_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float part[16];
     if (a.q) pdl_launch_dependents();      // a product behind this kernel may set itself up meanwhile
+    constexpr int E = Unit<DT>::E, N = CH * 8 / E;
     const int lane = threadIdx.x & 31;
     const int threads = WARP ? 32 : blockDim.x;
     const int t = WARP ? lane : threadIdx.x;
     const int64_t row = WARP ? int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= a.tokens) return;      // whole warps (a CTA always has its row)
-    float h[CH][8];
+    float h[N][E];
     float ss = 0.f;
-    constexpr bool VEC = HOW != kSingle;
     const int ph = HOW == kPhased ? int((row * a.ldx) & 7) : 0;
-    const int stride = VEC ? threads * 8 : threads;      // between a thread's columns j and j + 1 (VEC) / elements
-    Raw8<DT> x[CH];
+    auto column = [&](int j) { return HOW == kSingle ? j * E * threads + t : (j * threads + t) * E - ph; };
+    Unit<DT> x[N];
 #pragma unroll
-    for (int j = 0; j < CH; ++j)
-        norm_load<DT, HOW>(a.x, row * a.ldx, a.cols, VEC ? j * stride + t * 8 - ph : j * 8 * stride + t, threads, x[j]);
+    for (int j = 0; j < N; ++j) norm_load<DT, HOW>(a.x, row * a.ldx, a.cols, column(j), threads, x[j]);
 #pragma unroll
-    for (int j = 0; j < CH; ++j) raw8_f32<DT>(x[j], h[j]);
+    for (int j = 0; j < N; ++j) x[j].f32(h[j]);
     if (a.r) {
+        constexpr int B = N < 8 ? N : 8;      // so many loads at once
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            Raw8<DT> raw;
-            float r[8];
-            norm_load<DT, HOW>(a.r, row * a.ldr, a.cols, VEC ? j * stride + t * 8 - ph : j * 8 * stride + t, threads, raw);
-            raw8_f32<DT>(raw, r);
+        for (int j0 = 0; j0 < N; j0 += B) {
+            Unit<DT> raw[B];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[j][i] += r[i];
+            for (int j = 0; j < B; ++j)
+                norm_load<DT, HOW>(a.r, row * a.ldr, a.cols, column(j0 + j), threads, raw[j]);
+#pragma unroll
+            for (int j = 0; j < B; ++j) {
+                float r[E];
+                raw[j].f32(r);
+#pragma unroll
+                for (int i = 0; i < E; ++i) h[j0 + j][i] += r[i];
+            }
         }
     }
 #pragma unroll
-    for (int j = 0; j < CH; ++j)
+    for (int j = 0; j < N; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(h[j][i], h[j][i], ss);
+        for (int i = 0; i < E; ++i) ss = fmaf(h[j][i], h[j][i], ss);
     ss = warp_sum(ss);
     if constexpr (!WARP) {
         if (lane == 0) part[threadIdx.x >> 5] = ss;
@@ -168,25 +251,24 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) rmsnorm_kernel(const __grid_
     }
     const float inv = rsqrtf(fmaf(ss, a.inv_cols, a.eps));
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-        if constexpr (VEC) {
-            const int c = j * stride + t * 8 - ph;
+    for (int j = 0; j < N; ++j) {
+        if constexpr (HOW != kSingle) {
+            const int c = column(j);
             const int n = a.cols - c;
-            const bool whole = HOW == kVec || (c >= 0 && n >= 8);
-            float w[8];
-            if (a.w) norm_weights(a, c, c < 0 ? -c : 0, n, w);
-            if (a.h) norm_store(a.h, DT, row * a.ldh + c, c, n, whole, h[j]);
+            float w[E];
+            if (a.w) norm_weights<E>(a, c, c < 0 ? -c : 0, n, w);
+            if (a.h) norm_store<E>(a.h, DT, row * a.ldh + c, c, n, h[j]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < E; ++i) {
                 const float y = h[j][i] * inv;
                 h[j][i] = i < n ? (a.w ? y * w[i] : y) : 0.f;
             }
-            if (a.y) norm_store(a.y, a.yt, row * a.ldy + c, c, n, whole, h[j]);
+            if (a.y) norm_store<E>(a.y, a.yt, row * a.ldy + c, c, n, h[j]);
             if (HOW == kVec && a.q) mx8_store_vec(a, row, c, h[j], c < a.span);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int c = (j * 8 + i) * threads + t;
+            for (int i = 0; i < E; ++i) {
+                const int c = column(j) + i * threads;
                 const bool in = c < a.cols;
                 if (a.h && in) store_rn(a.h, DT, row * a.ldh + c, h[j][i]);
                 float y = in ? h[j][i] * inv : 0.f;
@@ -209,7 +291,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) rmsnorm_kernel(const __grid_
 // The weights stay in registers, loaded once: a load behind the stores waited
 // thousands of cycles in the saturated memory pipeline.  So a CTA's rows have
 // one phase, the grid being a multiple of eight CTAs (10007 x 5001 in fp32 74
-// us, with weights loaded for every row 94; registers bounded so that the CTAs
+// us in a fp32 ring, with weights loaded for every row 94; registers bounded so that the CTAs
 // the launch counts on fit).  A row held in registers between its two passes
 // beats one read twice from its stage by fewer warps (4096 x 4096 in 16 bits 24
 // against 34 us: half the unpacking).
@@ -247,7 +329,7 @@ __global__ void __launch_bounds__(CH == 1 ? 256 : 512, CH == 1 ? 6 : CH == 2 ? 2
     for (int j = 0; j < CH; ++j) {
         const int c = (j * threads + t) * 8 - ph;
         if (a.w) {
-            norm_weights(a, c, c < 0 ? -c : 0, a.cols - c, w[j]);
+            norm_weights<8>(a, c, c < 0 ? -c : 0, a.cols - c, w[j]);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[j][i] = 1.0f;
@@ -368,7 +450,7 @@ int launch_norm_ring(NormArgs& a, cudaStream_t st, bool& taken) {
     // and 30.5)
     const int ch = chunks <= 256 ? 1 : chunks <= 1024 ? 2 : 4;
     const int threads = ((chunks + ch - 1) / ch + 31) / 32 * 32;
-    // CTAs of an SM by its registers (20,000 x 400 in 16 bits: 24 of them 15 us, 8 of them 19); two stages each
+    // CTAs of an SM by its registers; two stages each
     auto room = [](int ctas) { return 228 * 1024 / ctas - 1536; };      // shared memory of each, static and reserved off
     int per_sm = (ch == 4 ? 512 : ch == 2 ? 1024 : 1536) / threads;
     if (per_sm < 1) per_sm = 1;
@@ -452,7 +534,7 @@ extern "C" int gale_rmsnorm(const void* x, const void* residual, int dtype, int6
                         agrees(y, ldy) && (!mx8 || ldx % 8 == 0);
     // The ring pays where a row costs many instructions per byte and there are rows enough: in 16 bits, from 1024
     // columns and 4.5 M elements on (with residual: 4736 x 4096 21 us, straight into registers 32; 20,000 x 704 20 each;
-    // 592 x 5000 5.9 and 5.2).  In fp32 registers are ahead everywhere (10,007 x 5000: 67 us, ring 78).
+    // 592 x 5000 5.9 and 5.2).  In fp32 registers are ahead everywhere (10,007 x 5000: 65 us, ring 78).
     if (phased && dtype != GALE_F32 && cols >= 1024 && tokens * cols >= 4500000) {
         bool taken = false;
         const int rc = dtype == GALE_BF16 ? launch_norm_ring<GALE_BF16>(a, st, taken)
