@@ -289,20 +289,24 @@ __device__ __noinline__ uint32_t exact_groups(const SelectArgs& a, int64_t t, in
 }
 
 // Keys with a bias as fixed point below the token's largest one, `hi`: the
-// fraction bits of key * scale + c in [1, 2), c = 1.9999 - hi * scale, keys
-// further down at 1 + 2^-23, masked ones at 1; over a bit that says the expert
-// exists and its index (inverted).  scale is 1, or the power of two that brings
-// the smallest key into the window where a pick lies below it.  23 bits (two less
-// for many experts) resolve what fp32 keys can tell, where the leading bits of a
-// float resolved 2^-16 and one token in ten had neighbouring picks in doubt.
+// fraction bits of key * scale + c in [1, 2), c = 1.9999 - hi * scale, over a bit
+// that says the expert exists and its index (inverted).  Keys further down have
+// the lowest fraction above 0 (kBelow: their order is in doubt), masked ones 0
+// (kMasked: theirs is the index's).  scale is 1, or the power of two that brings
+// the smallest key into the window where a pick lies below it.  23 bits (22 and 21
+// beyond 256 and 512 experts, whose index takes more) resolve what fp32 keys can
+// tell, where the leading bits of a float resolved 2^-16 and one token in ten had
+// neighbouring picks in doubt.
 template <int V>
 struct Fixed {
     static constexpr uint32_t kIndex = 32 * V - 1;
     static constexpr int kLow = V <= 8 ? 9 : V == 16 ? 10 : 11;     // index and existence bits
-    static constexpr float kUnit = 1.1920929e-7f * (1 << (kLow - 9));
+    static constexpr float kUnit = 1.1920929e-7f * (1 << (kLow - 9));   // one step of a fraction
+    static constexpr int kMasked = 0, kBelow = 1;
     static __device__ __forceinline__ uint32_t pack(float key, float scale, float c, int e) {
         // (c's rounding may carry the largest keys of a large bias to 2: they tie below it, in doubt)
-        const float f = key == kMinusInf ? 1.0f : fminf(fmaxf(fmaf(key, scale, c), 1.0000001f), 1.9999999f);
+        const float f = key == kMinusInf ? 1.0f + kMasked * kUnit
+                                           : fminf(fmaxf(fmaf(key, scale, c), 1.0f + kBelow * kUnit), 1.9999999f);
         return ((__float_as_uint(f) << 9) & ~((1u << kLow) - 1u)) | (1u << (kLow - 1)) | (kIndex - e);
     }
     static __device__ __forceinline__ int expert(uint32_t m) { return int(kIndex - (m & kIndex)); }
@@ -346,7 +350,7 @@ __device__ __noinline__ bool refine(const SelectArgs& a, int64_t t, int lane, in
     }
     // a key that is not among the n is at most the last one's
     const float most = 1.0f + float(F::fraction(last) + 1) * F::kUnit - c;      // (in the window's scale)
-    return last == 0u || F::fraction(last) == 0 || fmaf(kth, scale, -most) > margin * scale;
+    return last == 0u || F::fraction(last) == F::kMasked || fmaf(kth, scale, -most) > margin * scale;
 }
 
 // The sum over lanes 0 .. K - 1 (zeros from K on), valid in those lanes.
@@ -647,10 +651,10 @@ __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_ke
                 id = F::expert(m);
                 // (margin in the window's scale, and the window's own rounding)
                 const float off = fmaf(margin, scale, 2.4e-7f);
-                const bool clear = lane >= a.K || next == 0u || F::fraction(next) == 0 ||
+                const bool clear = lane >= a.K || next == 0u || F::fraction(next) == F::kMasked ||
                                    float(F::fraction(m) - F::fraction(next) - 1) * F::kUnit > off;
                 if (__all_sync(0xffffffffu, clear)) break;
-                if (scale == 1.0f && __any_sync(0xffffffffu, lane <= a.K && m != 0u && F::fraction(m) == 1)) {
+                if (scale == 1.0f && __any_sync(0xffffffffu, lane <= a.K && m != 0u && F::fraction(m) == F::kBelow)) {
                     float lo = INFINITY;
 #pragma unroll
                     for (int j = 0; j < V; ++j) lo = stays(lane + 32 * j) && s[j] > kMinusInf ? fminf(lo, s[j]) : lo;

@@ -197,3 +197,92 @@ def test_select_many_tokens():
         g = s.gather(1, ids.long())
         g = 2.5 * g / g.sum(-1, keepdim=True)
         assert torch.allclose(gates.double(), g, rtol=2e-5, atol=0)
+
+
+# beyond 256 experts a packed key's fraction gives bits to the index
+MANY = [(257, (1, 1, 1)), (384, (8, 3, 2)), (512, (16, 5, 1)), (1024, (32, 7, 2))]
+
+
+@pytest.mark.parametrize("E,groups", MANY)
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_select_many_experts_below_the_window(E, groups, sigmoid):
+    # keys more than a window of one below the largest are ordered too
+    for shape in {(1, 1, 1), groups}:
+        l = _logits(24, E, E)
+        l[:, 100] = 20.0                         # one logit leads, no bias to speak of
+        _run(l, 6, torch.zeros(E, device="cuda"), sigmoid, shape)
+        l, b = _logits(24, E, E + 1), torch.zeros(E, device="cuda")
+        b[100] = 2.0                             # one expert is wanted by its bias
+        _run(l, 6, b, sigmoid, shape)
+        l = 100.0 * l                            # saturated scores
+        _run(l, 6, b, sigmoid, shape)
+
+
+@pytest.mark.parametrize("E,groups", MANY)
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("lead", [0.05, 1.03, 3.0])
+def test_select_many_experts_behind_masks(E, groups, sigmoid, lead):
+    # ten live experts at high indices: none of the masked ones below them is picked first
+    l = torch.full((16, E), -float("inf"), device="cuda")
+    live = list(range(E - 50, E, 5))
+    l[:, live] = -4.0 + 0.1 * _logits(16, 10, 3)
+    b = torch.zeros(E, device="cuda")
+    b[live[3]] = lead
+    for shape in {(1, 1, 1), groups}:
+        _run(l, 6, b, sigmoid, shape)
+        _run(l, 12, b, sigmoid, shape)           # fewer live ones than picks
+
+
+@pytest.mark.parametrize("E,groups", MANY)
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_select_many_experts_wide_and_large_biases(E, groups, sigmoid):
+    l = _logits(24, E, 12)
+    for shape in {(1, 1, 1), groups}:
+        for spread in (0.5, 2.0, 30.0, 1e4, 1e20):
+            b = _bias(E, 13, spread)
+            _run(l, 8, b, sigmoid, shape)
+            b[::2] = -1e9
+            _run(l, 16, b, sigmoid, shape)
+        for offset in (-3e3, 1e3, 1e5, 1e7, 1e15, 2.5e38):
+            _run(l, 8, (_bias(E, 15, 0.3).double() + offset).float(), sigmoid, shape)
+
+
+@pytest.mark.parametrize("E,groups", MANY)
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_select_many_experts_near_ties(E, groups, sigmoid):
+    rng = np.random.default_rng(E)
+    l = np.full((24, E), 1.5, dtype=np.float32)
+    l = (l.view(np.int32) + rng.integers(-2, 3, size=l.shape).astype(np.int32)).view(np.float32)
+    l[:, ::2] = rng.normal(size=l[:, ::2].shape)
+    b = np.full(E, 0.25, dtype=np.float32)
+    b = (b.view(np.int32) + rng.integers(-2, 3, size=E).astype(np.int32)).view(np.float32)
+    b[::3] = 0.0
+    lt, bt = torch.from_numpy(l).cuda(), torch.from_numpy(b).cuda()
+    for shape in {(1, 1, 1), groups}:
+        _run(lt, 8, bt, sigmoid, shape)
+        _run(lt.bfloat16(), 8, bt, sigmoid, shape)
+        bt2 = bt.clone()
+        bt2[7] = 3.0                             # the ties lie below the window
+        _run(lt, 8, bt2, sigmoid, shape)
+
+
+@pytest.mark.parametrize("E,groups", MANY)
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_select_many_experts_masks_and_extremes(E, groups, sigmoid, dtype):
+    l = _logits(9, E, 1, dtype)
+    inf, big = float("inf"), float(torch.finfo(DT[dtype]).max)
+    l[0] = -inf
+    l[1, 3:] = -inf
+    l[2, ::2] = -inf
+    l[3, :E // 2] = -big
+    l[4, 9] = inf
+    l[5] = 0.0
+    l[6] = 100.0 * l[6]
+    l[7] = -200.0 + l[7]
+    l[8, :E - 3] = float("nan")
+    b = _bias(E, 2)
+    b[E // 2] = -inf
+    for shape in {(1, 1, 1), groups}:
+        for bias in (None, b):
+            _run(l, 6, bias, sigmoid, shape)
