@@ -19,7 +19,10 @@
 //
 // PAIR: two CTAs share a tile of 256 rows.  Either holds its own 128 rows and
 // half of the tokens' bytes, so a CTA's shared memory takes in 24 KB instead of
-// 40 KB per 128 x 128 x 256 products; the first CTA issues for both.
+// 40 KB per 128 x 128 x 256 products; the first CTA issues for both.  The second
+// CTA's copies complete on the first one's barriers, which is what orders them
+// before the MMAs that read them: a warp that waited for them and passed the news
+// on would need a release at cluster scope for every stage.
 //
 // RESIDENT (up to 128 tokens, rows up to 8192 columns): the tokens' scales of all
 // the CTA's columns are copied to TMEM once.  Copying them with every stage cost
@@ -196,13 +199,15 @@ __device__ __forceinline__ void gemm_join(const GemmArgs& a, const GemmUnit& w, 
 template <bool PAIR, bool RESIDENT>
 __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_constant__ CUtensorMap wmap,
                                                               const __grid_constant__ CUtensorMap xmap,
+                                                              const __grid_constant__ CUtensorMap wscmap,
+                                                              const __grid_constant__ CUtensorMap xscmap,
                                                               const __grid_constant__ GemmArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align1024(smem_raw);
-    // full: a stage's bytes are here (two producers); peer: they are in the pair's other CTA too;
-    // empty: its MMAs are done; acc_full: a unit's accumulators are final; acc_free: the columns that
-    // the next unit's buffer shares with them have been read
-    __shared__ uint64_t full[kGMaxStages], peer[PAIR ? kGMaxStages : 1], empty[kGMaxStages], acc_full[2], acc_free, res_full;
+    // full: a stage's bytes are here, and in the pair's other CTA (two producers; of a pair the first CTA's
+    // alone is used); empty: its MMAs are done; acc_full: a unit's accumulators are final; acc_free: the columns
+    // that the next unit's buffer shares with them have been read
+    __shared__ uint64_t full[kGMaxStages], empty[kGMaxStages], acc_full[2], acc_free, res_full;
     __shared__ uint32_t tmem_base;
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     const int rank = PAIR ? int(blockIdx.x & 1) : 0;
@@ -210,7 +215,6 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
         for (int s = 0; s < a.stages; ++s) {
             mbar_init(&full[s], 2);
             mbar_init(&empty[s], 1);
-            if (PAIR) mbar_init(&peer[s], 1);
         }
         mbar_init(&acc_full[0], 1);
         mbar_init(&acc_full[1], 1);
@@ -222,6 +226,10 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
         if (lane == 0) {
             prefetch_tensormap(&wmap);
             prefetch_tensormap(&xmap);
+            if (PAIR) {
+                prefetch_tensormap(&wscmap);
+                prefetch_tensormap(&xscmap);
+            }
         }
         __syncwarp();
         if (PAIR) {
@@ -242,13 +250,14 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
     bool ok = true;
     GemmUnit w;
     const uint32_t ring = smem_u32(smem), ring_end = ring + a.stages * a.stage_bytes;
-    const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), peer0 = smem_u32(peer);
+    const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
     if (warp == 0 || warp == 2) {
         const bool lead = elect_one();
         int issued = 0;
         // (st, s8: the stage's shared memory and the offset of its barriers)
         uint32_t st = ring, s8 = 0, phase = 1;      // of the empty barriers: the first turn of the ring passes
         const int atoms_all = int((a.tokens + kMxTile - 1) / kMxTile);
+        const uint32_t landed0 = PAIR ? cluster_address(full0, 0) : full0;      // where the copies complete
         if (RESIDENT && warp == 2) {
             int k0, k1;
             gemm_columns<PAIR>(a, k0, k1);
@@ -266,12 +275,30 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
             const uint8_t* xsc = a.xsc + int64_t(atom0) * a.nt * kMxAtomBytes;
             const int line = rt * a.nt * kMxTile;
             for (int k = w.k0; k < w.k1; k += kGK) {
-                ok = mbar_wait_warp(empty0 + s8, phase);
+                ok = mbar_wait_warp<PAIR>(empty0 + s8, phase);
                 if (!ok) break;
                 const int kt = min(kGK, w.k1 - k);
                 const uint32_t bar = full0 + s8;
                 const uint32_t sc = st + kGK * (kGABytes + xbytes);
-                if (warp == 0) {
+                if (PAIR && warp == 0) {
+                    // (the first CTA expects the bytes of both; scales come two atoms at a time)
+                    if (rank == 0)
+                        mbar_expect_lead(lead, bar, 2 * (kt * kMx4TileBytes + kGK * kMxAtomBytes));
+                    tma_load_2d_pair(lead, st, &wmap, landed0 + s8, 0, line + k * kMxTile);
+                    if (kt == 2)
+                        tma_load_2d_pair(lead, st + kGABytes, &wmap, landed0 + s8, 0, line + (k + 1) * kMxTile);
+                    tma_load_2d_pair(lead, sc, &wscmap, landed0 + s8, 0, min(rt, a.rtiles - 1) * a.nt + k);
+                } else if (PAIR) {
+                    const uint32_t xs = st + kGK * kGABytes;
+                    if (rank == 0)
+                        mbar_expect_lead(lead, bar, 2 * (kt * xbytes + atoms * kGK * kMxAtomBytes));
+                    tma_load_2d_pair(lead, xs, &xmap, landed0 + s8, k * kMxTile, t0 + rank * xrows);
+                    if (kt == 2)
+                        tma_load_2d_pair(lead, xs + xbytes, &xmap, landed0 + s8, (k + 1) * kMxTile, t0 + rank * xrows);
+                    for (int j = 0; j < atoms; ++j)
+                        tma_load_2d_pair(lead, sc + (1 + j) * kGK * kMxAtomBytes, &xscmap, landed0 + s8, 0,
+                                         (atom0 + j) * a.nt + k);
+                } else if (warp == 0) {
                     // the spread weights count with their packed bytes
                     mbar_expect_lead(lead, bar, kt * (kMx4TileBytes + kMxAtomBytes));
                     tma_load_2d(lead, st, &wmap, bar, 0, line + k * kMxTile);
@@ -280,8 +307,8 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
                 } else {
                     const uint32_t xs = st + kGK * kGABytes;
                     mbar_expect_lead(lead, bar, kt * (xbytes + atoms * kMxAtomBytes));
-                    tma_load_2d(lead, xs, &xmap, bar, k * kMxTile, t0 + rank * xrows);
-                    if (kt == 2) tma_load_2d(lead, xs + xbytes, &xmap, bar, (k + 1) * kMxTile, t0 + rank * xrows);
+                    tma_load_2d(lead, xs, &xmap, bar, k * kMxTile, t0);
+                    if (kt == 2) tma_load_2d(lead, xs + xbytes, &xmap, bar, (k + 1) * kMxTile, t0);
                     for (int j = 0; j < atoms; ++j)
                         bulk_load_lead(lead, sc + (1 + j) * kGK * kMxAtomBytes,
                                        xsc + (int64_t(j) * a.nt + k) * kMxAtomBytes, kt * kMxAtomBytes, bar);
@@ -297,9 +324,9 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
             }
         }
         // before the CTA may end (bounded): the last stages' MMAs have reported, or after a failure the last
-        // copies have landed
-        for (int i = max(0, issued - a.stages); i < issued; ++i)
-            ok = mbar_wait_warp((ok ? empty0 : full0) + i % a.stages * 8, (i / a.stages) & 1) && ok;
+        // copies have landed (a pair's first CTA waits for both CTAs', the second one for it at the cluster's barrier)
+        for (int i = max(0, issued - a.stages); i < issued && (!PAIR || rank == 0 || ok); ++i)
+            ok = mbar_wait_warp<PAIR>((ok ? empty0 : full0) + i % a.stages * 8, (i / a.stages) & 1) && ok;
     } else if (warp == 1 && (!PAIR || rank == 0)) {
         const bool lead = elect_one();
         const uint32_t idesc = umma_idesc_mx(PAIR ? 2 * kMxTile : kMxTile, a.n);
@@ -329,7 +356,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
                 tc_fence_after();
             }
             for (int k = w.k0; k < w.k1; k += kGK) {
-                ok = mbar_wait_warp(full0 + s8, phase) && (!PAIR || mbar_wait_warp<true>(peer0 + s8, phase));
+                ok = mbar_wait_warp<PAIR>(full0 + s8, phase);
                 if (!ok) break;
                 tc_fence_after();
                 const int kt = min(kGK, w.k1 - k);
@@ -373,27 +400,11 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
             if (PAIR) umma_commit_pair(lead, &acc_full[u & 1]);
             else umma_commit_one(lead, &acc_full[u & 1]);
         }
-    } else if (PAIR && warp == 1) {
-        // second CTA of the pair: passes on that its stages have landed
-        uint32_t s8 = 0, phase = 0;
-        for (int u = 0; ok && gemm_unit<PAIR>(a, u, w); ++u) {
-            for (int k = w.k0; k < w.k1; k += kGK) {
-                ok = mbar_wait_warp(full0 + s8, phase);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_cluster_relaxed(peer0 + s8, 0);
-                __syncwarp();
-                s8 += 8;
-                if (s8 == uint32_t(a.stages) * 8) {
-                    s8 = 0;
-                    phase ^= 1;
-                }
-            }
-        }
     } else if (warp >= 4) {
         const int quarter = warp & 3;
         const uint32_t lanes = uint32_t(quarter) << 21;
         for (int u = 0; ok && gemm_unit<PAIR>(a, u, w); ++u) {
-            ok = mbar_wait_warp(smem_u32(&acc_full[u & 1]), (u >> 1) & 1);
+            ok = mbar_wait_warp<PAIR>(smem_u32(&acc_full[u & 1]), (u >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + lanes + ((u & 1) ? a.d1 : 0);
@@ -416,7 +427,7 @@ __global__ void __launch_bounds__(kGThreads, 1) mx_gemm_kernel(const __grid_cons
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (PAIR) mbar_arrive_cluster_relaxed(smem_u32(&acc_free), 0);
+                    if (PAIR && rank) mbar_arrive_cluster(smem_u32(&acc_free), 0);
                     else mbar_arrive(&acc_free);
                 }
             };
@@ -630,9 +641,11 @@ extern "C" int gale_mx_gemm(const void* w4, int64_t rows, int64_t cols, const vo
     p.a.status = static_cast<int32_t*>(ws);
     p.a.ldy = ldy;
     p.a.ydtype = y_dtype;
-    CUtensorMap wmap, xmap;
+    CUtensorMap wmap, xmap, wscmap{}, xscmap{};      // (the scales' maps: pairs only)
     int rc = make_map_mx4(&wmap, w, W.q_bytes / (kMxTile / 2));
     if (rc == GALE_OK) rc = make_map_bytes(&xmap, x, W.cols_padded, tokens, kMxTile, p.pair ? p.a.n / 2 : p.a.n);
+    if (rc == GALE_OK && p.pair) rc = make_map_atoms(&wscmap, p.a.wsc, W.s_bytes / kMxAtomBytes);
+    if (rc == GALE_OK && p.pair) rc = make_map_atoms(&xscmap, p.a.xsc, X.s_bytes / kMxAtomBytes);
     if (rc != GALE_OK) return rc;
     p.a.pair16 = ldy % 2 == 0 && aligned(y, 4);
     auto kern = p.pair ? mx_gemm_kernel<true, false> : p.resident ? mx_gemm_kernel<false, true> : mx_gemm_kernel<false, false>;
@@ -650,7 +663,7 @@ extern "C" int gale_mx_gemm(const void* w4, int64_t rows, int64_t cols, const vo
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kern, wmap, xmap, p.a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kern, wmap, xmap, wscmap, xscmap, p.a) != cudaSuccess) {
         cudaGetLastError();      // reported here, not by the next call
         return GALE_ERR_CUDA;
     }

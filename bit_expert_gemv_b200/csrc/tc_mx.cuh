@@ -87,13 +87,11 @@ __device__ __forceinline__ void tmem_copy_scales_pair(bool lead, uint32_t taddr,
         "l"(desc), "r"(uint32_t(lead))
         : "memory");
 }
-// Arrive on the barrier at this address in CTA `rank` of the cluster, without
-// release (which takes 700 cycles at cluster scope): for an arrival that passes
-// on what the caller's own wait has made sure of.
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar, uint32_t rank) {
+// Arrive on the barrier at this address in CTA `rank` of the cluster, with release.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar, uint32_t rank) {
     uint32_t remote;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(bar), "r"(rank));
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 
 // A 512-byte scale atom (32 rows of 16 bytes, 8-row groups 128 bytes apart, no
@@ -126,8 +124,8 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// One try of an mbarrier phase; CLUSTER: with acquire at cluster scope (the
-// arrival came from the pair's other CTA).
+// One try of an mbarrier phase; CLUSTER: with acquire at cluster scope (an
+// arrival may come from the pair's other CTA).
 template <bool CLUSTER>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -161,6 +159,25 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
         ok = __all_sync(0xffffffffu, ok);
     }
     return ok;
+}
+
+// The address of the barrier at `bar` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_address(uint32_t bar, uint32_t rank) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(bar), "r"(rank));
+    return remote;
+}
+// 2-D tiled TMA load into this CTA's shared memory that completes on a barrier of
+// the pair's first CTA (`bar`: its cluster address; no multicast).
+__device__ __forceinline__ void tma_load_2d_pair(bool lead, uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0,
+                                                 int c1) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3}], [%4];\n\t}"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar), "r"(uint32_t(lead))
+        : "memory");
 }
 
 // 2-D tiled TMA load into shared memory, completing on `bar` (no multicast).

@@ -53,6 +53,21 @@ int make_map_mx4(CUtensorMap* m, const void* base, int64_t lines) {
     return r == CUDA_SUCCESS ? GALE_OK : GALE_ERR_CUDA;
 }
 
+// Scale atoms of 512 bytes as lines of 128 words, boxes of two neighbouring
+// atoms, as they lie in memory; lines past the last read as zero.
+int make_map_atoms(CUtensorMap* m, const void* base, int64_t atoms) {
+    auto fn = encode_fn();
+    if (!fn) return GALE_ERR_CUDA;
+    cuuint64_t dims[2] = {128, cuuint64_t(atoms)};
+    cuuint64_t strides[1] = {512};
+    cuuint32_t box[2] = {128, 2};
+    cuuint32_t es[2] = {1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GALE_OK : GALE_ERR_CUDA;
+}
+
 // A [rows][pitch] byte matrix, boxes of box_cols x box_rows, 128-byte swizzle;
 // rows past the last read as zero.
 int make_map_bytes(CUtensorMap* m, const void* base, int64_t pitch, int64_t rows, int box_cols, int box_rows) {

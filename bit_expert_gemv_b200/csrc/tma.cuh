@@ -11,6 +11,7 @@ constexpr int kTileRows = 16;   // rows of one MMA tile (and of one TMA box)
 int make_map_3d(CUtensorMap* m, bool u16, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                 uint64_t stride1, uint64_t stride2, uint32_t b0, uint32_t b1, bool swizzle128);
 int make_map_mx4(CUtensorMap* m, const void* base, int64_t lines);
+int make_map_atoms(CUtensorMap* m, const void* base, int64_t atoms);
 int make_map_bytes(CUtensorMap* m, const void* base, int64_t pitch, int64_t rows, int box_cols, int box_rows);
 int make_sign_map(CUtensorMap* m, const void* first_matrix, int rows, int cols, int experts, int64_t stride);
 int make_scale_map(CUtensorMap* m, const void* first_matrix, int rows, int cols, int experts, int64_t stride);

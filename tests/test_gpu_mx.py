@@ -254,3 +254,25 @@ def test_gemm_behind_copies_and_other_kernels():
     for _ in range(4):
         g.replay()
     check()
+
+
+@pytest.mark.parametrize("rows,cols,tokens", [(3900, 1600, 1100), (16400, 900, 600), (8192, 2100, 513), (130, 4000, 9000)])
+def test_gemm_pairs_repeat_under_load(rows, cols, tokens):
+    """Tiles over CTA pairs: odd numbers of row tiles, of column tiles and of
+    tokens, several tiles per pair, and the same bits from call to call while
+    another stream keeps the memory busy (what one CTA copies or frees, the other
+    one's MMAs read or overwrite)."""
+    w, x = _matrix(rows, cols, rows, scale=0.02), _matrix(tokens, cols, tokens, "bf16", 3.0)
+    w4, x8 = _pack4(w), _pack8(x)
+    first = _gemm(w4, rows, cols, x8, tokens, "f32")
+    _check(first, *_want(w, x), cols, "f32")
+    s, noise = torch.cuda.Stream(), torch.zeros(1 << 26, device="cuda")
+    ws = torch.zeros(G.gale_mx_gemm_workspace_size(rows, cols, tokens), dtype=torch.uint8, device="cuda")
+    ys = [torch.empty(tokens, rows, device="cuda") for _ in range(12)]
+    torch.cuda.synchronize()
+    for y in ys:
+        with torch.cuda.stream(s):
+            noise.add_(1.0)
+        G.gale_mx_gemm(w4, rows, cols, x8, y, ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, first) for y in ys) and int(ws[:4].view(torch.int32).item()) == 0
