@@ -1,20 +1,22 @@
 // Host-side entry points with no kernels: status strings, the packed-matrix
 // layout and the per-device attribute cache.
+#include <atomic>
+
 #include "common.cuh"
 
 namespace gale {
 
 int sm_count() {
-    static int cached[64] = {0};
+    static std::atomic<int> cached[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-    if (cached[dev] == 0) {
-        int n = 0;
+    int n = cached[dev];
+    if (n == 0) {
         if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
             n = 148;
         cached[dev] = n;
     }
-    return cached[dev];
+    return n;
 }
 
 }  // namespace gale

@@ -31,6 +31,8 @@
 // Without PAIR, the tiles that are left after whole rounds are split over the
 // columns by a cluster of up to 8 CTAs, whose partial sums are added through
 // distributed shared memory in rank order.
+#include <atomic>
+
 #include "mx.cuh"
 #include "tc_mx.cuh"
 #include "tma.cuh"
@@ -489,12 +491,12 @@ struct GemmPlan {
 // Clusters of `size` CTAs of this kernel that the device holds at once (an SM
 // that is left over in its group of SMs holds none of a larger cluster).
 int gemm_clusters(int size) {
-    static int found[64][4] = {};       // per device, by log2 of the size: an attribute of the device
+    static std::atomic<int> found[64][4];       // per device, by log2 of the size: an attribute of the device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     const int slot = size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : 3;
-    if (!found[dev][slot]) {
-        int n = 0;
+    int n = found[dev][slot];
+    if (!n) {
         if (ensure_smem(reinterpret_cast<const void*>(mx_gemm_kernel<false, false>), kGSmemSm) != GALE_OK) return 0;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(unsigned(size) * 16);
@@ -511,7 +513,7 @@ int gemm_clusters(int size) {
         }
         found[dev][slot] = n;
     }
-    return found[dev][slot];
+    return n;
 }
 
 // Chooses the tile's tokens, pairs or single CTAs and the split of left-over tiles

@@ -2,6 +2,8 @@
 // driver entry point, so the library does not link libcuda directly).
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "tma.cuh"
 
@@ -9,14 +11,15 @@ namespace gale {
 
 namespace {
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> found{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 fn = found;
     if (!fn) {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
         if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
             q != cudaDriverEntryPointSuccess)
             return nullptr;
-        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        found = fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
     }
     return fn;
 }
@@ -206,24 +209,6 @@ int cached_map(CUtensorMap* out, bool scale, const void* first_matrix, int rows,
     g_maps[g_map_next] = e;
     g_map_next = (g_map_next + 1) % kMapCache;
     *out = e.map;
-    return GALE_OK;
-}
-
-int ensure_smem(const void* kernel, int bytes) {
-    constexpr int kMaxDev = 64, kMaxKernels = 32;
-    static const void* kernels[kMaxDev][kMaxKernels] = {};
-    static int set_bytes[kMaxDev][kMaxKernels] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return GALE_ERR_CUDA;
-    int slot = -1;
-    for (int i = 0; i < kMaxKernels; ++i) {
-        if (kernels[dev][i] == kernel) { slot = i; break; }
-        if (!kernels[dev][i]) { slot = i; kernels[dev][i] = kernel; break; }
-    }
-    if (slot >= 0 && set_bytes[dev][slot] >= bytes) return GALE_OK;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-        return GALE_ERR_CUDA;
-    if (slot >= 0) set_bytes[dev][slot] = bytes;
     return GALE_OK;
 }
 

@@ -146,3 +146,57 @@ def test_blocks_on_two_streams(layer):
     for b, w in zip(blocks, want):
         for x, y in zip(b.outputs(), w):
             assert torch.equal(x, y)
+
+
+def test_two_threads_alternate_small_and_large_shapes():
+    """Two Python threads in the library at once, each on its own stream: products
+    and norms whose shared memory differs from call to call."""
+    import threading
+
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    jobs = []
+    for rows, cols, tokens in ((130, 200, 3), (2048, 4096, 300), (512, 512, 64), (300, 7000, 17)):
+        w = torch.empty(G.gale_mx4_layout(rows, cols).total, dtype=torch.uint8, device="cuda")
+        x = torch.empty(G.gale_mx8_layout(tokens, cols).total, dtype=torch.uint8, device="cuda")
+        G.gale_mx4_quantize(torch.randn(rows, cols, device="cuda"), w)
+        G.gale_mx8_quantize(torch.randn(tokens, cols, device="cuda"), x)
+        n = G.gale_mx_gemm_workspace_size(rows, cols, tokens)
+        jobs.append((lambda y, ws, w=w, x=x, rows=rows, cols=cols: G.gale_mx_gemm(w, rows, cols, x, y, ws), (tokens, rows),
+                     torch.float32, n))
+    for cols in (1024, 4096, 9000):
+        x = torch.randn(5000000 // cols, cols, device="cuda").bfloat16()
+        jobs.append((lambda y, ws, x=x: G.gale_rmsnorm(x, y=y), tuple(x.shape), torch.bfloat16, 256))
+
+    def run_all(order):
+        out = {}
+        for i in order:
+            call, shape, dtype, n = jobs[i]
+            y, ws = torch.zeros(shape, dtype=dtype, device="cuda"), torch.zeros(n, dtype=torch.uint8, device="cuda")
+            call(y, ws)
+            out[i] = y
+        return out
+
+    errors, got = [], {}
+
+    def work(name, order):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(25):
+                    got[name] = run_all(order)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:
+            errors.append(e)
+
+    torch.cuda.synchronize()
+    n = len(jobs)
+    threads = [threading.Thread(target=work, args=a) for a in (("a", range(n)), ("b", range(n - 1, -1, -1)))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    want = run_all(range(n))
+    torch.cuda.synchronize()
+    for out in got.values():
+        assert all(torch.equal(out[i], want[i]) for i in range(n))
