@@ -530,7 +530,8 @@ extern "C" int gale_rmsnorm(const void* x, const void* residual, int dtype, int6
     // bases on 16 bytes and row strides that agree modulo 8 elements: rows in aligned chunks (with MXFP8, whose blocks
     // start with the row, only if rows start on chunks of eight)
     auto agrees = [&](const void* p, int64_t ld) { return !p || (aligned(p, 16) && (ld - ldx) % 8 == 0); };
-    const bool phased = a.span > 256 && agrees(x, ldx) && agrees(residual, ldr) && agrees(sum_out, ldsum) &&
+    // (and a row with the chunk that its phase may add has to fit 512 threads of 64 columns)
+    const bool phased = a.span > 256 && a.span <= kNormMaxCols - 8 && agrees(x, ldx) && agrees(residual, ldr) && agrees(sum_out, ldsum) &&
                         agrees(y, ldy) && (!mx8 || ldx % 8 == 0);
     // The ring pays where a row costs many instructions per byte and there are rows enough: in 16 bits, from 1024
     // columns and 4.5 M elements on (with residual: 4736 x 4096 21 us, straight into registers 32; 20,000 x 704 20 each;

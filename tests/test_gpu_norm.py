@@ -196,3 +196,19 @@ def test_norm_graph_on_another_stream():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("cols,ld", [(32760, 32769), (32761, 32761), (32764, 32771), (32768, 32769), (32768, 32770)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("tokens", [2, 9])
+def test_norm_widest_rows_at_any_start(cols, ld, dtype, out, tokens):
+    # with the columns before its first aligned ones such a row takes more than 512 threads' share
+    x, r = _rand((tokens, ld), cols, dtype)[:, :cols], _rand((tokens, ld), 2, dtype)[:, :cols]
+    w = 1 + 0.1 * _rand((cols,), 3, "f32")
+    y = torch.full((tokens, ld), 9.0, dtype=DT[out], device="cuda")
+    h = torch.full((tokens, ld), 9.0, dtype=DT[dtype], device="cuda")
+    G.gale_rmsnorm(x, y=y[:, :cols], residual=r, weight=w, sum_out=h[:, :cols])
+    hw, yw = M.rmsnorm(x.double().cpu().numpy(), r.double().cpu().numpy(), w.double().cpu().numpy())
+    _close(h[:, :cols], hw, dtype)
+    _close(y[:, :cols], yw, out)
+    assert (y[:, cols:] == 9).all() and (h[:, cols:] == 9).all()
