@@ -239,10 +239,17 @@ __global__ void __maxnreg__(CH == 1 ? 40 : CH == 2 ? 48 : CH == 4 ? 64 : 128) rm
             }
         }
     }
+    // no more than 32 squares are added in order: an addition may lose half a unit of the sum
+    constexpr int kRun = N * E <= 32 ? N : 32 / E;
 #pragma unroll
-    for (int j = 0; j < N; ++j)
+    for (int j0 = 0; j0 < N; j0 += kRun) {
+        float part_ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < E; ++i) ss = fmaf(h[j][i], h[j][i], ss);
+        for (int j = j0; j < j0 + kRun; ++j)
+#pragma unroll
+            for (int i = 0; i < E; ++i) part_ss = fmaf(h[j][i], h[j][i], part_ss);
+        ss += part_ss;
+    }
     ss = warp_sum(ss);
     if constexpr (!WARP) {
         if (lane == 0) part[threadIdx.x >> 5] = ss;

@@ -212,3 +212,18 @@ def test_norm_widest_rows_at_any_start(cols, ld, dtype, out, tokens):
     _close(h[:, :cols], hw, dtype)
     _close(y[:, :cols], yw, out)
     assert (y[:, cols:] == 9).all() and (h[:, cols:] == 9).all()
+
+
+@pytest.mark.parametrize("cols", [16384, 20480, 32768])
+@pytest.mark.parametrize("first", [0, 1, 2, 3])
+def test_norm_sum_order_of_wide_rows(cols, first):
+    """Squares just below half a unit of a thread's first one: each addition in
+    order loses one whole, so a thread that added 64 of them in order would be
+    off by 63 half units.  32 in order are what the bound above allows."""
+    x = torch.full((2, cols), 2.0 ** -12 * (1 - 2.0 ** -12), device="cuda")
+    x[:, first:2048:4] = 1.0                    # every thread's first column, whatever its unit
+    x[1] *= 1.25
+    w = 1 + _rand((cols,), 5, "f32").abs().clamp(max=0.99)
+    y = torch.empty_like(x)
+    G.gale_rmsnorm(x, y=y, weight=w, eps=0.0)
+    _close(y, M.rmsnorm(x.double().cpu().numpy(), None, w.double().cpu().numpy(), 0.0)[1], "f32")
