@@ -361,23 +361,30 @@ __device__ __forceinline__ T picks_sum(int K, T v) {
 }
 
 // Gates of the picks (lane k holds pick k and its logit `l`), written with the ids.  `lmax` and
-// `sum`: the softmax's maximum and denominator, read where they are needed.
+// `sum`: the softmax's maximum and denominator, read where they are needed.  The fast
+// exponential's error grows with its argument, here a pick's distance from the largest logit,
+// so expf (no slower: 65,536 tokens 32.8 us with either).  (The denominator's fast
+// exponentials weigh with their own size: 8 units of it at most.)  The fast quotients are good
+// to 2 units while the divisor is normal and below 2^126, which all of these are; true ones
+// took 2 us more.
 __device__ __forceinline__ void write_picks(const SelectArgs& a, int64_t t, int lane, int id, float l, float lmax,
                                             float sum) {
     const bool on = lane < a.K;
     if (!on) l = kMinusInf;
     float g, z;
     if (a.sigmoid) {
-        g = __fdividef(1.0f, 1.0f + __expf(-l));      // 0 past the last pick
+        // (by the exponential that cannot overflow: scores down to the smallest fp32 keep their digits)
+        const float e = expf(-fabsf(l));
+        g = __fdividef(l < 0.f ? e : 1.0f, 1.0f + e);      // 0 past the last pick
         if (a.renorm) {
             z = picks_sum(a.K, g);
-            if (__any_sync(0xffffffffu, on && z < 1e-30f)) {
-                // scores at the end of fp32's range: their ratios in 64 bits
+            if (__any_sync(0xffffffffu, on && g < 1.17549435e-38f && l > kMinusInf && z < 0.25f)) {
+                // subnormal scores have lost digits that a small sum brings to light: their ratios in 64 bits
                 const double d = l == kMinusInf ? 0.0 : 1.0 / (1.0 + exp(-double(l)));
                 const double zd = picks_sum(a.K, d);
                 g = zd > 0.0 ? float(d / zd) : 0.f;
             } else {
-                g = __fdividef(g, z);
+                g = z > 0.f ? __fdividef(g, z) : 0.f;
             }
         }
     } else if (a.renorm) {
@@ -385,11 +392,11 @@ __device__ __forceinline__ void write_picks(const SelectArgs& a, int64_t t, int 
         float m = l;
         if (a.bias) m = warp_max_f(l);
         else m = __shfl_sync(0xffffffffu, l, 0);
-        g = __expf(l - fmaxf(m, -kFltMax));
+        g = expf(l - fmaxf(m, -kFltMax));
         z = picks_sum(a.K, g);
         g = z > 0.f ? __fdividef(g, z) : 0.f;
     } else {
-        g = sum > 0.f ? __fdividef(__expf(l - lmax), sum) : 0.f;
+        g = sum > 0.f ? __fdividef(expf(l - lmax), sum) : 0.f;
     }
     if (on) {
         const int64_t at = t * a.K + lane;

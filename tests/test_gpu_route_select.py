@@ -286,3 +286,35 @@ def test_select_many_experts_masks_and_extremes(E, groups, sigmoid, dtype):
     for shape in {(1, 1, 1), groups}:
         for bias in (None, b):
             _run(l, 6, bias, sigmoid, shape)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_select_gates_of_far_picks(dtype):
+    """Gates to within what their own formula rounds, also of picks far below the
+    largest logit and of scores near the smallest fp32.  Sigmoid: the exponential
+    2 units, the sum half, a quotient 2: the score of a pick 4.5, the sum of at
+    most 16 of them 4.5 and its additions 2, the last quotient 2, together 13.
+    Softmax: half a unit of the argument's size |x| as well, in the pick's own
+    exponential (|x| / 2 + 2) and, weighed by exp(-|x|) |x| < 1, in the sum (0.5 +
+    2 + 2), with the quotient |x| / 2 + 9; the denominator over all experts 8 units
+    and 10 for its additions: |x| / 2 + 22.  A subnormal result is off by its own
+    rounding too."""
+    l = torch.full((64, 64), -300.0, device="cuda")
+    pick = -torch.from_numpy(np.random.default_rng(3).uniform(0, 103, size=(64, 8)).astype(np.float32)).cuda()
+    pick[:, 0] = 0.0
+    l[:, 5:61:7] = pick
+    l = l.to(DT[dtype])
+    l[:32] -= 60.0                                # the sigmoids of half of the tokens: all tiny
+    l64 = l.double().cpu().numpy()
+    for sigmoid in (False, True):
+        for renorm in (False, True):
+            ids = torch.empty(64, 8, dtype=torch.int32, device="cuda")
+            gates = torch.empty(64, 8, device="cuda")
+            G.gale_route_select(l, ids, gates, score=G.GALE_SCORE_SIGMOID if sigmoid else G.GALE_SCORE_SOFTMAX,
+                                renorm=renorm)
+            want_ids, want = R.route_select(l64, None, 8, sigmoid, renorm=renorm)
+            assert np.array_equal(ids.cpu().numpy(), want_ids)
+            x = l64.max(1, keepdims=True) - np.take_along_axis(l64, want_ids, 1)
+            units = 13.0 if sigmoid else 0.5 * x + (9.0 if renorm else 22.0)
+            off = np.abs(gates.double().cpu().numpy() - want)
+            assert (off <= units * 2.0 ** -23 * want + 4 * 2.0 ** -149).all(), (sigmoid, renorm)
