@@ -618,9 +618,9 @@ __global__ void __launch_bounds__(256, select_ctas<V, SCORED>()) route_select_ke
             const bool in = (kept >> lane) & 1u;
             const float worst = -warp_max_f(in ? -score : kMinusInf);
             const float best = warp_max_f(lane < a.groups && !in ? score : kMinusInf);
-            // (a sum of two finite keys that leaves fp32's range tells nothing)
+            // (a sum of two finite keys that leaves fp32's range, to either side, tells nothing)
             sure = certain(worst, best, 2.0f * es + 4.8e-7f * big) &&
-                   !__any_sync(0xffffffffu, score > kFltMax && k1 <= kFltMax);
+                   !__any_sync(0xffffffffu, isinf(score) && !isinf(k1));
             if (!sure && !a.bias) {
                 // the best two of a group are certain (by logit): their scores in 64 bits
                 const double all = a.sigmoid ? 1.0 : softmax_sum64<V>(l, lmax);

@@ -318,3 +318,21 @@ def test_select_gates_of_far_picks(dtype):
             units = 13.0 if sigmoid else 0.5 * x + (9.0 if renorm else 22.0)
             off = np.abs(gates.double().cpu().numpy() - want)
             assert (off <= units * 2.0 ** -23 * want + 4 * 2.0 ** -149).all(), (sigmoid, renorm)
+
+
+@pytest.mark.parametrize("E", [64, 256, 1024])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_select_group_sums_below_fp32(E, sigmoid):
+    # experts pushed out by the lowest finite biases: the sum of two leaves fp32, but their groups come before
+    # masked ones, and before each other by the 64-bit sums
+    low, size = float(torch.finfo(torch.float32).min), E // 8
+    l = _logits(6, E, 4)
+    l[:, :size] = -float("inf")                  # group 0 is masked
+    b = torch.full((E,), low, device="cuda")
+    b[5 * size:6 * size] = 0.0                   # one group as it should be
+    _run(l, size + 4 if size < 12 else 12, b, sigmoid, (8, 2, 2))
+    b[5 * size:6 * size] = low
+    b[3 * size:4 * size] = 0.98 * low
+    b[6 * size:7 * size] = 0.97 * low
+    for keep in (1, 2, 3, 7):
+        _run(l, 8, b, sigmoid, (8, keep, 2))
