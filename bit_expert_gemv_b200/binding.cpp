@@ -84,14 +84,26 @@ struct Call {
         if (device < 0) throw Refused{"tensors on a CUDA device"};
         if (device != int(c10::cuda::current_device())) throw Refused{"tensors on the current device"};
         if (o == Py_None) return c10::cuda::getCurrentCUDAStream(c10::DeviceIndex(device)).stream();
-        if (PyLong_Check(o)) return PyLong_AsVoidPtr(o);
+        if (PyLong_Check(o)) return handle(o);
         PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
         if (!h) {
             PyErr_Clear();
             throw Refused{"a stream"};
         }
-        void* p = PyLong_AsVoidPtr(h);
+        void* p = nullptr;
+        const bool good = PyLong_Check(h);
+        if (good) p = PyLong_AsVoidPtr(h);
         Py_DECREF(h);
+        if (!good) throw Refused{"a stream"};
+        return checked(p);
+    }
+    static void* handle(PyObject* o) { return checked(PyLong_AsVoidPtr(o)); }
+    // no Python error may be left behind by a call that goes on
+    static void* checked(void* p) {
+        if (!p && PyErr_Occurred()) {
+            PyErr_Clear();
+            throw Refused{"a stream"};
+        }
         return p;
     }
 };
@@ -103,6 +115,14 @@ int64_t whole(PyObject* o) {
         throw Refused{"an integer"};
     }
     return v;
+}
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {
+        PyErr_Clear();
+        throw Refused{"a truth value"};
+    }
+    return v != 0;
 }
 float real(PyObject* o) {
     const double v = PyFloat_AsDouble(o);
@@ -158,7 +178,7 @@ PyObject* route_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (bias) Call::flat(bias, at::kFloat, E);
         const int dt = logits.dtype();
         const int score = int(whole(a[4])), groups = int(whole(a[5])), keep = int(whole(a[6])), top = int(whole(a[7]));
-        const int renorm = PyObject_IsTrue(a[8]) == 1;
+        const int renorm = truth(a[8]);
         const float scale = real(a[9]);
         void* s = c.stream(a[10]);
         return unlocked([&] {
