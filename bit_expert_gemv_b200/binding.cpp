@@ -116,6 +116,11 @@ int64_t whole(PyObject* o) {
     }
     return v;
 }
+int whole32(PyObject* o) {
+    const int64_t v = whole(o);
+    if (v < INT32_MIN || v > INT32_MAX) throw Refused{"an integer of 32 bits"};
+    return int(v);
+}
 bool truth(PyObject* o) {
     const int v = PyObject_IsTrue(o);
     if (v < 0) {
@@ -177,7 +182,7 @@ PyObject* route_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Call::flat(gates, at::kFloat, B * K);
         if (bias) Call::flat(bias, at::kFloat, E);
         const int dt = logits.dtype();
-        const int score = int(whole(a[4])), groups = int(whole(a[5])), keep = int(whole(a[6])), top = int(whole(a[7]));
+        const int score = whole32(a[4]), groups = whole32(a[5]), keep = whole32(a[6]), top = whole32(a[7]);
         const int renorm = truth(a[8]);
         const float scale = real(a[9]);
         void* s = c.stream(a[10]);

@@ -41,3 +41,14 @@ def test_streams_that_are_no_handles():
             G.gale_route_select(l, ids, gates, stream=stream)
     torch.cuda.synchronize()
     assert (ids == -7).all()
+
+
+@pytest.mark.parametrize("name", ["score", "n_groups", "keep_groups", "group_top"])
+@pytest.mark.parametrize("offset", [1 << 32, -1 << 32, 1 << 62])
+def test_integers_beyond_32_bits(name, offset):
+    # 2^32 + 1 is not 1
+    l, ids, gates = _router()
+    with pytest.raises(G.GaleError):
+        G.gale_route_select(l, ids, gates, **{name: offset + 1})
+    torch.cuda.synchronize()
+    assert (ids == -7).all()
