@@ -30,8 +30,9 @@ struct Refused {
 // A tensor argument, or none.
 struct Arg {
     const at::Tensor* t = nullptr;
+    void* data = nullptr;      // read with the tensor: a tensor without memory of its own raises
     explicit operator bool() const { return t != nullptr; }
-    void* ptr() const { return t ? t->data_ptr() : nullptr; }
+    void* ptr() const { return data; }
     int64_t size(int i) const { return t->size(i); }
     int dtype() const {
         switch (t->scalar_type()) {
@@ -55,6 +56,7 @@ struct Call {
         const int d = a.t->is_cuda() ? int(a.t->get_device()) : -2;
         if (device == -1) device = d;
         else if (device != d) throw Refused{"tensors on one device"};
+        a.data = a.t->data_ptr();
         return a;
     }
     // [rows, cols] whose rows are contiguous: the row stride in elements
@@ -159,13 +161,16 @@ PyObject* guarded(const char* name, Py_ssize_t have, Py_ssize_t want, F f) {
     Py_RETURN_NONE;
 }
 
-// The library's call, with other Python threads running meanwhile (a full launch queue blocks).
+// The library's call, with other Python threads running meanwhile (a full launch queue
+// blocks).  `f` touches no Python object and no tensor; should it throw all the same, the
+// exception is handled with the interpreter's lock held.
 template <typename F>
 int unlocked(F f) {
-    PyThreadState* state = PyEval_SaveThread();
-    const int rc = f();
-    PyEval_RestoreThread(state);
-    return rc;
+    struct Lock {
+        PyThreadState* state = PyEval_SaveThread();
+        ~Lock() { PyEval_RestoreThread(state); }
+    } lock;
+    return f();
 }
 
 PyObject* route_select(PyObject*, PyObject* const* a, Py_ssize_t n) {

@@ -1,5 +1,8 @@
 """What the compiled argument marshalling does with arguments of the right kind
 but a wrong value: it refuses them, whole, before the library is called."""
+import subprocess
+import sys
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -52,3 +55,30 @@ def test_integers_beyond_32_bits(name, offset):
         G.gale_route_select(l, ids, gates, **{name: offset + 1})
     torch.cuda.synchronize()
     assert (ids == -7).all()
+
+
+TRACED = """
+import torch, bit_expert_gemv_b200 as G
+x = torch.randn(3, 4, 64, device="cuda")
+y = torch.zeros(4, 64, device="cuda")
+ids = torch.zeros(4, 6, dtype=torch.int32, device="cuda")
+def norm(v):
+    G.gale_rmsnorm(v, y=y)
+    return v
+def router(v):
+    G.gale_route_select(v, ids, torch.zeros(4, 6, device="cuda"))
+    return v
+for f in (norm, router):
+    try:
+        torch.func.vmap(f)(x)
+    except RuntimeError as e:
+        print("refused")
+torch.cuda.synchronize()
+assert not y.any()
+"""
+
+
+def test_tensors_without_memory_of_their_own():
+    # (in a process of its own: an exception while other threads may run would end it)
+    r = subprocess.run([sys.executable, "-c", TRACED], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split() == ["refused", "refused"], r.stderr[-2000:]
