@@ -53,6 +53,8 @@ struct Call {
         Arg a;
         a.t = &THPVariable_Unpack(o);
         if (!a.t->defined() || a.t->layout() != at::kStrided) throw Refused{"a dense tensor"};
+        // (a view that negates when read: its memory holds the other sign)
+        if (a.t->is_neg()) throw Refused{"a tensor without a pending negation"};
         const int d = a.t->is_cuda() ? int(a.t->get_device()) : -2;
         if (device == -1) device = d;
         else if (device != d) throw Refused{"tensors on one device"};

@@ -82,3 +82,13 @@ def test_tensors_without_memory_of_their_own():
     # (in a process of its own: an exception while other threads may run would end it)
     r = subprocess.run([sys.executable, "-c", TRACED], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.split() == ["refused", "refused"], r.stderr[-2000:]
+
+
+def test_lazily_negated_tensors():
+    # the sign is a flag of the view, not in memory
+    x = torch.randn(4, 64, device="cuda")
+    y, (l, ids, gates) = torch.empty_like(x), _router()
+    for call in (lambda: G.gale_rmsnorm(torch._neg_view(x), y=y), lambda: G.gale_rmsnorm(x, y=torch._neg_view(y)),
+                 lambda: G.gale_route_select(torch._neg_view(l), ids, gates)):
+        with pytest.raises(G.GaleError):
+            call()
