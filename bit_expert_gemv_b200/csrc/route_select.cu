@@ -721,7 +721,7 @@ extern "C" int gale_route_select(const void* logits, int logits_dtype, int64_t l
     // exact quotients: e * (gmagic * gsize - 2^20) < 2^20 for e < 1024, gsize <= 1024
     a.gmagic = ((1u << 20) + gsize - 1) / gsize;
     cudaStream_t st = as_stream(stream);
-    const unsigned grid = unsigned((B + 7) / 8);
+    const unsigned grid = unsigned((int64_t(B) + 7) / 8);
     auto launch = [&](auto v) {
         constexpr int V = decltype(v)::value;
         if (a.bias || a.groups > 1) route_select_kernel<V, true><<<grid, 256, 0, st>>>(a);

@@ -336,3 +336,16 @@ def test_select_group_sums_below_fp32(E, sigmoid):
     b[6 * size:7 * size] = 0.97 * low
     for keep in (1, 2, 3, 7):
         _run(l, 8, b, sigmoid, (8, keep, 2))
+
+
+def test_select_as_many_tokens_as_an_int_counts():
+    B = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GB")
+    l = torch.zeros(B, 1, dtype=torch.float16, device="cuda")
+    ids = torch.full((B, 1), 7, dtype=torch.int32, device="cuda")
+    gates = torch.full((B, 1), 7.0, device="cuda")
+    G.gale_route_select(l, ids, gates)
+    step = 1 << 28
+    for t in range(0, B, step):
+        assert not ids[t:t + step].any() and (gates[t:t + step] == 1.0).all()
