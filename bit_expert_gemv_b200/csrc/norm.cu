@@ -29,7 +29,7 @@ struct NormArgs {
     int64_t tokens;
     int64_t nt;          // padded columns / 128
     int cols, span;      // span: columns written (the padded ones with MXFP8)
-    int dt, wt, yt;
+    int wt, yt;
     int vw;              // w may be read 16 bytes at a time
     float inv_cols;
     int stages, stage_bytes, r_off;      // ring: stages, bytes of one, where the residual's row starts in it
@@ -297,9 +297,8 @@ __global__ void __maxnreg__(CH == 1 ? 40 : CH == 2 ? 48 : CH == 4 ? 64 : 128) rm
 //
 // The weights stay in registers, loaded once: a load behind the stores waited
 // thousands of cycles in the saturated memory pipeline.  So a CTA's rows have
-// one phase, the grid being a multiple of eight CTAs (10007 x 5001 in fp32 74
-// us in a fp32 ring, with weights loaded for every row 94; registers bounded so that the CTAs
-// the launch counts on fit).  A row held in registers between its two passes
+// one phase, the grid being a multiple of eight CTAs; registers are bounded so that
+// the CTAs the launch counts on fit.  A row held in registers between its two passes
 // beats one read twice from its stage by fewer warps (4096 x 4096 in 16 bits 24
 // against 34 us: half the unpacking).
 template <int DT, int CH, bool PHASED>
@@ -307,7 +306,8 @@ __global__ void __launch_bounds__(CH == 1 ? 256 : 512, CH == 1 ? 6 : CH == 2 ? 2
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ float part[2][16];
     __shared__ uint64_t full[8];
-    constexpr int ES = DT == GALE_F32 ? 4 : 2;
+    static_assert(DT != GALE_F32, "16-bit rows");
+    constexpr int ES = 2;
     if (a.q) pdl_launch_dependents();
     const int lane = threadIdx.x & 31, t = threadIdx.x, threads = blockDim.x;
     if (t == 0) {
@@ -349,9 +349,9 @@ __global__ void __launch_bounds__(CH == 1 ? 256 : 512, CH == 1 ? 6 : CH == 2 ? 2
         uint8_t* st = ring + s * a.stage_bytes;
         if (row + 1 == a.tokens && (ph + a.cols) * ES % 16) {      // what the copy left out
             for (int e = ((ph + a.cols) * ES & ~15) / ES + t; e < ph + a.cols; e += threads) {
-                using T = std::conditional_t<DT == GALE_F32, uint32_t, uint16_t>;
-                reinterpret_cast<T*>(st)[e] = static_cast<const T*>(a.x)[row * a.ldx - ph + e];
-                if (a.r) reinterpret_cast<T*>(st + a.r_off)[e] = static_cast<const T*>(a.r)[row * a.ldr - ph + e];
+                reinterpret_cast<uint16_t*>(st)[e] = static_cast<const uint16_t*>(a.x)[row * a.ldx - ph + e];
+                if (a.r)
+                    reinterpret_cast<uint16_t*>(st + a.r_off)[e] = static_cast<const uint16_t*>(a.r)[row * a.ldr - ph + e];
             }
             __syncthreads();
         }
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(CH == 1 ? 256 : 512, CH == 1 ? 6 : CH == 2 ? 2
                 if (a.h) store8(a.h, DT, row * a.ldh + c, 8, true, h[j]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * inv * w[j][i];
-                if (DT != GALE_F32 && a.y && a.yt == DT) store8(a.y, DT, row * a.ldy + c, 8, true, h[j]);
+                if (a.y && a.yt == DT) store8(a.y, DT, row * a.ldy + c, 8, true, h[j]);
                 else if (a.y) store8(a.y, a.yt, row * a.ldy + c, 8, true, h[j]);
             } else {
 #pragma unroll
@@ -517,7 +517,6 @@ extern "C" int gale_rmsnorm(const void* x, const void* residual, int dtype, int6
     a.tokens = tokens;
     a.cols = int(cols);
     a.span = int(cols);
-    a.dt = dtype;
     a.wt = w_dtype;
     a.yt = y_dtype;
     a.eps = eps;

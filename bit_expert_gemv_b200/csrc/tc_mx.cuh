@@ -87,10 +87,15 @@ __device__ __forceinline__ void tmem_copy_scales_pair(bool lead, uint32_t taddr,
         "l"(desc), "r"(uint32_t(lead))
         : "memory");
 }
+// The cluster's address of what CTA `rank` has at this shared-memory address.
+__device__ __forceinline__ uint32_t cluster_address(uint32_t addr, uint32_t rank) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+    return remote;
+}
 // Arrive on the barrier at this address in CTA `rank` of the cluster, with release.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar, uint32_t rank) {
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(bar), "r"(rank));
+    const uint32_t remote = cluster_address(bar, rank);
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 
@@ -161,12 +166,6 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
     return ok;
 }
 
-// The address of the barrier at `bar` in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t cluster_address(uint32_t bar, uint32_t rank) {
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(bar), "r"(rank));
-    return remote;
-}
 // 2-D tiled TMA load into this CTA's shared memory that completes on a barrier of
 // the pair's first CTA (`bar`: its cluster address; no multicast).
 __device__ __forceinline__ void tma_load_2d_pair(bool lead, uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0,
@@ -207,11 +206,6 @@ __device__ __forceinline__ void mbar_expect_lead(bool lead, uint32_t bar, uint32
         : "memory");
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -222,9 +216,8 @@ __device__ __forceinline__ void cluster_sync_relaxed() {
 }
 // Four floats at the same shared-memory address in CTA `rank` of the cluster.
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr, uint32_t rank) {
-    uint32_t remote;
+    const uint32_t remote = cluster_address(addr, rank);
     float4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                  : "r"(remote)
