@@ -199,10 +199,10 @@ __device__ __forceinline__ void norm_store(void* p, int dtype, int64_t at, int c
 // thread: (j * threads + t) * E + i less the row's phase, or, kSingle, (j * E +
 // i) * threads + t.  Units of 16 bytes in fp32 too, so that a warp's access is
 // one run of 512 bytes; all of a row's loads, then all of its residual's, are
-// asked for before the first is used (10,007 x 5000 fp32: 67 -> 65 us, with
-// residual 95 -> 88).  Registers are bounded for as many CTAs as keep HBM busy:
+// asked for before the first is used (10,007 x 5000 fp32: 67 -> 62 us, with
+// residual 95 -> 89).  Registers are bounded for as many CTAs as keep HBM busy:
 // 50 instead of 48 of them for two chunks cost a fourth CTA at 5000 columns, 74
-// us.
+// us.  (Chosen on rows in units: kSingle spills 20 to 650 bytes a thread under them.)
 template <int DT, int HOW, int CH, bool WARP>
 __global__ void __maxnreg__(CH == 1 ? 40 : CH == 2 ? 48 : CH == 4 ? 64 : 128) rmsnorm_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float part[16];
@@ -541,7 +541,7 @@ extern "C" int gale_rmsnorm(const void* x, const void* residual, int dtype, int6
                         agrees(y, ldy) && (!mx8 || ldx % 8 == 0);
     // The ring pays where a row costs many instructions per byte and there are rows enough: in 16 bits, from 1024
     // columns and 4.5 M elements on (with residual: 4736 x 4096 21 us, straight into registers 32; 20,000 x 704 20 each;
-    // 592 x 5000 5.9 and 5.2).  In fp32 registers are ahead everywhere (10,007 x 5000: 65 us, ring 78).
+    // 592 x 5000 5.9 and 5.2).  In fp32 registers are ahead everywhere (10,007 x 5000: 62 us, ring 78).
     if (phased && dtype != GALE_F32 && cols >= 1024 && tokens * cols >= 4500000) {
         bool taken = false;
         const int rc = dtype == GALE_BF16 ? launch_norm_ring<GALE_BF16>(a, st, taken)

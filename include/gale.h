@@ -218,9 +218,12 @@ int gale_route_topk(const float* logits, int B, int E, int K, int32_t* ids, floa
  * it adds nothing to its group's score (a group of masked experts has -inf).  Every
  * finite logit is scored, the type's lowest too; +inf counts as the largest
  * finite fp32.  Where too few experts are left, masked ones are picked with
- * gate 0; a token whose picks' scores are all 0 has gates 0.  A NaN s_e + bias
- * counts as -inf.  The order is that of the 64-bit values of these formulas;
- * gates are fp32.
+ * gate 0; a token whose picks are all masked, or whose sigmoids are all 0 in 64
+ * bits, has gates 0.  (Renormalised softmax gates are taken relative to the
+ * largest pick, so picks that the bias finds far below the largest logit share
+ * the scale as well.)  A NaN s_e + bias counts as -inf.  The order is that of the
+ * 64-bit values of these formulas; gates are fp32, to within a few units and
+ * half a unit per step of (largest logit - l).
  *   logits : device [B][E] of logits_dtype (GALE_F32, GALE_BF16, GALE_F16),
  *            rows ld elements apart (ld >= E)
  *   bias   : device fp32 [E], or NULL
