@@ -200,3 +200,74 @@ def test_two_threads_alternate_small_and_large_shapes():
     torch.cuda.synchronize()
     for out in got.values():
         assert all(torch.equal(out[i], want[i]) for i in range(n))
+
+
+def _last_rows_only(make, rows, cols, dtype):
+    """A [rows, cols] tensor whose last 3 rows alone hold values."""
+    t = torch.zeros(rows, cols, dtype=dtype, device="cuda")
+    t[-3:] = make((3, cols)).to(dtype)
+    return t
+
+
+@pytest.mark.parametrize("cols", [700, 4096, 4097, 32768])
+def test_norm_offsets_beyond_32_bits(cols):
+    if not torch.cuda.is_available() or torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    rows = 2 ** 31 // cols + 9
+    x = _last_rows_only(lambda s: _normal(s, 71), rows, cols, torch.bfloat16)
+    r = _last_rows_only(lambda s: _normal(s, 72), rows, cols, torch.bfloat16)
+    y, h = torch.full_like(x, 5.0), torch.full_like(x, 5.0)
+    G.gale_rmsnorm(x, y=y, residual=r, sum_out=h)
+    tail = [torch.empty(3, cols, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    G.gale_rmsnorm(x[-3:].clone(), y=tail[0], residual=r[-3:].clone(), sum_out=tail[1])
+    hw, yw = M.rmsnorm(x[-3:].double().cpu().numpy(), r[-3:].double().cpu().numpy())
+    for got, few, want in ((y, tail[0], yw), (h, tail[1], hw)):
+        tol = np.abs(want) * (30 * 2.0 ** -24 + 2.0 ** -8) + 1e-30       # as in the norm's own tests
+        assert (np.abs(got[-3:].double().cpu().numpy() - want) <= tol).all()
+        assert (np.abs(few.double().cpu().numpy() - want) <= tol).all()
+        assert not got[:-3].any()
+
+
+def test_product_offsets_beyond_32_bits():
+    if not torch.cuda.is_available() or torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    rows, cols, tokens = 40000, 130, 2 ** 31 // 40000 + 9
+    w, x = _normal((rows, cols), 73), _last_rows_only(lambda s: _normal(s, 74), tokens, cols, torch.bfloat16)
+    w4 = torch.empty(G.gale_mx4_layout(rows, cols).total, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(G.gale_mx_gemm_workspace_size(rows, cols, tokens), dtype=torch.uint8, device="cuda")
+    G.gale_mx4_quantize(w, w4)
+    out = []
+    for part in (x, x[-3:].clone()):
+        x8 = torch.empty(G.gale_mx8_layout(part.shape[0], cols).total, dtype=torch.uint8, device="cuda")
+        G.gale_mx8_quantize(part, x8)
+        out.append(torch.full((part.shape[0], rows), 5.0, dtype=torch.bfloat16, device="cuda"))
+        G.gale_mx_gemm(w4, rows, cols, x8, out[-1], ws)
+    wv = torch.empty(rows, cols, device="cuda")
+    G.gale_mx4_unpack(w4, wv)                                          # exact in fp32
+    xv = torch.from_numpy(M.values(*M.quantize(x[-3:].double().cpu().numpy(), M.GRID8), M.GRID8)).cuda()
+    want, mag = xv @ wv.double().t(), xv.abs() @ wv.double().abs().t()
+    tol = (cols / 32 + 34) * 2.0 ** -23 * mag + want.abs() * 2.0 ** -8 * (1 + 1e-6)      # as in the product's own tests
+    for got in (out[0][-3:], out[1]):
+        assert ((got.double() - want).abs() <= tol).all()
+    assert not out[0][:-3].any() and int(ws[:4].view(torch.int32).item()) == 0
+
+
+def test_microscaled_offsets_beyond_32_bits():
+    if not torch.cuda.is_available() or torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    for cols in (4096, 4097):
+        rows = (2 ** 31 // cols + 9) // 128 * 128 + 131          # 3 rows in the last tile
+        w = _last_rows_only(lambda s: _normal(s, 75), rows, cols, torch.bfloat16)
+        back, few = torch.full_like(w, 5.0), torch.empty(3, cols, dtype=torch.bfloat16, device="cuda")
+        for src, dst in ((w, back), (w[-3:].clone(), few)):
+            p = torch.empty(G.gale_mx4_layout(src.shape[0], cols).total, dtype=torch.uint8, device="cuda")
+            G.gale_mx4_quantize(src, p)
+            G.gale_mx4_unpack(p, dst)
+        assert torch.equal(back[-3:], few) and few.any() and not back[:-3].any()
+        L, L3 = G.gale_mx8_layout(rows, cols), G.gale_mx8_layout(3, cols)
+        p, p3 = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in (L.total, L3.total))
+        G.gale_mx8_quantize(w, p)
+        G.gale_mx8_quantize(w[-3:].clone(), p3)
+        assert torch.equal(p[L.q_bytes - 3 * L.cols_padded:L.q_bytes], p3[:L3.q_bytes])
+        assert not p[:L.q_bytes - 3 * L.cols_padded].any()
+        del w, back, p
